@@ -299,6 +299,159 @@ int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, const flo
                           static_cast<cudaStream_t>(stream));
 }
 
+// Shape of the attention within molecules (supported set stated in egat.h).
+static int check_mol_shape(const egat_mol_shape* s) {
+  if (!s) return EGAT_ERR_ARG;
+  if (s->nq < 0 || s->nk < 0 || s->n_mol < 0) return EGAT_ERR_ARG;
+  if (s->dtype != EGAT_F32 && s->dtype != EGAT_BF16) return EGAT_ERR_ARG;
+  if (s->cap != 0.f && !(s->cap >= 1e-30f && s->cap <= 3.0e38f)) return EGAT_ERR_ARG;
+  if (s->lmax < 0 || s->lmax > kMaxL) return EGAT_ERR_UNSUPPORTED;
+  if (s->C != 16 && s->C != 32 && s->C != 64 && s->C != 128) return EGAT_ERR_UNSUPPORTED;
+  if (!pow2(s->H) || s->C % s->H != 0 || (s->C / s->H) % 8 != 0) return EGAT_ERR_UNSUPPORTED;
+  if (s->dk != 8 && s->dk != 16 && s->dk != 32) return EGAT_ERR_UNSUPPORTED;
+  if (s->H * s->dk > 256) return EGAT_ERR_UNSUPPORTED;
+  if (s->nq > (1 << 30) || s->nk > (1 << 30) || s->n_mol > (1 << 28)) return EGAT_ERR_UNSUPPORTED;
+  return EGAT_OK;
+}
+
+// Arguments common to the forward and backward pass; fills a.
+static int check_mol_args(const egat_mol_shape& s, const void* d_q, const void* d_k,
+                          const void* d_hp, const int32_t* d_q_ptr, const int32_t* d_k_ptr,
+                          const float* d_pos_q, const float* d_pos_k, const float* d_slope,
+                          MolArgs& a) {
+  if (!d_q_ptr || !aligned4(d_q_ptr) || !aligned4(d_k_ptr)) return EGAT_ERR_ARG;
+  if (!d_k_ptr && (s.nk != s.nq || d_pos_k)) return EGAT_ERR_ARG;
+  if ((s.nq > 0 && !d_q) || (s.nk > 0 && (!d_k || !d_hp))) return EGAT_ERR_ARG;
+  if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_hp)) return EGAT_ERR_ARG;
+  if (d_slope) {
+    if (s.nq > 0 && !d_pos_q) return EGAT_ERR_ARG;
+    if (d_k_ptr && s.nk > 0 && !d_pos_k) return EGAT_ERR_ARG;
+    if (!aligned4(d_pos_q) || !aligned4(d_pos_k) || !aligned4(d_slope)) return EGAT_ERR_ARG;
+  }
+  a.q = d_q;
+  a.k = d_k;
+  a.hp = d_hp;
+  a.qptr = d_q_ptr;
+  a.kptr = d_k_ptr ? d_k_ptr : d_q_ptr;
+  a.posq = d_pos_q;
+  a.posk = d_k_ptr ? d_pos_k : d_pos_q;
+  a.slope = d_slope;
+  a.self = !d_k_ptr;
+  return EGAT_OK;
+}
+
+int egat_molecule_attention_workspace_bytes(const egat_mol_shape* s, size_t* bytes) {
+  const int rc = check_mol_shape(s);
+  if (rc != EGAT_OK) return rc;
+  if (!bytes) return EGAT_ERR_ARG;
+  *bytes = molecule_ws_bytes(*s);
+  return EGAT_OK;
+}
+
+int egat_molecule_attention(const egat_mol_shape* s, const void* d_q, const void* d_k,
+                            const void* d_hp, const int32_t* d_q_ptr, const int32_t* d_k_ptr,
+                            const float* d_pos_q, const float* d_pos_k, const float* d_slope,
+                            void* d_ws, size_t ws_bytes, void* d_m, float* d_lse, void* stream) {
+  int rc = check_mol_shape(s);
+  if (rc != EGAT_OK) return rc;
+  MolArgs a;
+  rc = check_mol_args(*s, d_q, d_k, d_hp, d_q_ptr, d_k_ptr, d_pos_q, d_pos_k, d_slope, a);
+  if (rc != EGAT_OK) return rc;
+  if (s->nq == 0) return EGAT_OK;
+  if (!d_m || !aligned16(d_m) || !aligned4(d_lse)) return EGAT_ERR_ARG;
+  const size_t need = molecule_ws_bytes(*s);
+  if (need > 0 && (!d_ws || !aligned16(d_ws))) return EGAT_ERR_ARG;
+  if (ws_bytes < need) return EGAT_ERR_WORKSPACE;
+  return launch_molecule_attention(*s, a, d_ws, d_m, d_lse, static_cast<cudaStream_t>(stream));
+}
+
+int egat_molecule_attention_backward_workspace_bytes(const egat_mol_shape* s, size_t* bytes) {
+  const int rc = check_mol_shape(s);
+  if (rc != EGAT_OK) return rc;
+  if (!bytes) return EGAT_ERR_ARG;
+  *bytes = molecule_backward_ws_bytes(*s);
+  return EGAT_OK;
+}
+
+int egat_molecule_attention_backward(
+    const egat_mol_shape* s, const void* d_q, const void* d_k, const void* d_hp,
+    const int32_t* d_q_ptr, const int32_t* d_k_ptr, const float* d_pos_q, const float* d_pos_k,
+    const float* d_slope, const void* d_m, const float* d_lse, const void* d_grad_m, void* d_ws,
+    size_t ws_bytes, void* d_dq, void* d_dk, void* d_dhp, float* d_dpos_q, float* d_dpos_k,
+    float* d_dslope, void* stream) {
+  int rc = check_mol_shape(s);
+  if (rc != EGAT_OK) return rc;
+  MolArgs a;
+  rc = check_mol_args(*s, d_q, d_k, d_hp, d_q_ptr, d_k_ptr, d_pos_q, d_pos_k, d_slope, a);
+  if (rc != EGAT_OK) return rc;
+  if (!d_slope && (d_dpos_q || d_dpos_k || d_dslope)) return EGAT_ERR_ARG;
+  if (!d_k_ptr && d_dpos_k) return EGAT_ERR_ARG;
+  if (s->nq > 0 && (!d_m || !d_lse || !d_grad_m || !d_dq)) return EGAT_ERR_ARG;
+  if (s->nk > 0 && (!d_dk || !d_dhp)) return EGAT_ERR_ARG;
+  if (!aligned16(d_m) || !aligned4(d_lse) || !aligned16(d_grad_m) || !aligned16(d_dq) ||
+      !aligned16(d_dk) || !aligned16(d_dhp) || !aligned4(d_dpos_q) || !aligned4(d_dpos_k) ||
+      !aligned4(d_dslope))
+    return EGAT_ERR_ARG;
+  const size_t need = molecule_backward_ws_bytes(*s);
+  if (need > 0 && (!d_ws || !aligned16(d_ws))) return EGAT_ERR_ARG;
+  if (ws_bytes < need) return EGAT_ERR_WORKSPACE;
+  const MolGrads g{d_m, d_lse, d_grad_m, d_dq, d_dk, d_dhp, d_dpos_q, d_dpos_k, d_dslope};
+  return launch_molecule_backward(*s, a, g, d_ws, static_cast<cudaStream_t>(stream));
+}
+
+static int check_norm(int64_t ld, int32_t n, int32_t width, int32_t dtype) {
+  if (n < 0 || width < 1) return EGAT_ERR_ARG;
+  if (dtype != EGAT_F32 && dtype != EGAT_BF16) return EGAT_ERR_ARG;
+  if (width > 16384) return EGAT_ERR_UNSUPPORTED;
+  return ld < width ? EGAT_ERR_ARG : EGAT_OK;
+}
+static bool aligned_elem(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (storage_bytes(dtype) - 1)) == 0;
+}
+
+int egat_layer_norm(const void* d_x, int64_t ldx, int32_t n, int32_t width, int32_t dtype,
+                    const float* d_weight, const float* d_bias, float eps, void* d_y, int64_t ldy,
+                    float* d_stats, void* stream) {
+  int rc = check_norm(ldx, n, width, dtype);
+  if (rc == EGAT_OK) rc = check_norm(ldy, n, width, dtype);
+  if (rc != EGAT_OK) return rc;
+  if (!(eps >= 0.f) || eps > 3.0e38f) return EGAT_ERR_ARG;
+  if (n == 0) return EGAT_OK;
+  if (!d_x || !d_y || !aligned_elem(d_x, dtype) || !aligned_elem(d_y, dtype)) return EGAT_ERR_ARG;
+  if (!aligned4(d_weight) || !aligned4(d_bias) || !aligned4(d_stats)) return EGAT_ERR_ARG;
+  return launch_layer_norm(d_x, ldx, n, width, dtype, d_weight, d_bias, eps, d_y, ldy, d_stats,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int egat_layer_norm_backward_workspace_bytes(int32_t n, int32_t width, size_t* bytes) {
+  if (!bytes || n < 0 || width < 1) return EGAT_ERR_ARG;
+  if (width > 16384) return EGAT_ERR_UNSUPPORTED;
+  *bytes = layer_norm_backward_ws_bytes(n, width);
+  return EGAT_OK;
+}
+
+int egat_layer_norm_backward(const void* d_x, int64_t ldx, int32_t n, int32_t width, int32_t dtype,
+                             const float* d_weight, const float* d_stats, const void* d_grad,
+                             int64_t ldg, void* d_ws, size_t ws_bytes, void* d_dx, int64_t lddx,
+                             float* d_dweight, float* d_dbias, void* stream) {
+  int rc = check_norm(ldx, n, width, dtype);
+  if (rc == EGAT_OK) rc = check_norm(ldg, n, width, dtype);
+  if (rc == EGAT_OK && d_dx) rc = check_norm(lddx, n, width, dtype);
+  if (rc != EGAT_OK) return rc;
+  if (n > 0 && (!d_x || !d_stats || !d_grad)) return EGAT_ERR_ARG;
+  if (!aligned_elem(d_x, dtype) || !aligned_elem(d_grad, dtype) || !aligned_elem(d_dx, dtype))
+    return EGAT_ERR_ARG;
+  if (!aligned4(d_weight) || !aligned4(d_stats) || !aligned4(d_dweight) || !aligned4(d_dbias))
+    return EGAT_ERR_ARG;
+  if (!d_dx && !d_dweight && !d_dbias) return EGAT_OK;
+  const size_t need = layer_norm_backward_ws_bytes(n, width);
+  if (need > 0 && (!d_ws || !aligned16(d_ws))) return EGAT_ERR_ARG;
+  if (ws_bytes < need) return EGAT_ERR_WORKSPACE;
+  return launch_layer_norm_backward(d_x, ldx, n, width, dtype, d_weight, d_stats, d_grad, ldg, d_ws,
+                                    d_dx, lddx, d_dweight, d_dbias,
+                                    static_cast<cudaStream_t>(stream));
+}
+
 int egat_gather_rows(const void* d_src, int64_t n_src, int64_t row_bytes, const int32_t* d_idx,
                      int64_t count, void* d_dst, void* stream) {
   if (n_src < 0 || count < 0 || row_bytes <= 0 || row_bytes % 16) return EGAT_ERR_ARG;

@@ -151,4 +151,35 @@ int launch_attention_tc(const egat_shape& s, bool fused, const void* d_q, const 
                         const void* d_hp, const void* d_plan, const float* d_w2, float* d_out,
                         cudaStream_t st);
 
+// Attention within each molecule (egat_mol_shape in egat.h).  Self form: kptr = qptr and
+// posk = posq.  slope NULL: no distance bias.
+struct MolArgs {
+  const void *q, *k, *hp;
+  const int32_t *qptr, *kptr;
+  const float *posq, *posk, *slope;
+  bool self;
+};
+struct MolGrads {
+  const void* m;
+  const float* lse;
+  const void* g;
+  void *dq, *dk, *dhp;
+  float *dposq, *dposk, *dslope;
+};
+size_t molecule_ws_bytes(const egat_mol_shape& s);
+int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d_ws, void* d_m,
+                              float* d_lse, cudaStream_t st);
+size_t molecule_backward_ws_bytes(const egat_mol_shape& s);
+int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const MolGrads& g,
+                             void* d_ws, cudaStream_t st);
+// Layer norm of strided rows and its backward pass.
+int launch_layer_norm(const void* d_x, long long ldx, int n, int width, int dtype,
+                      const float* d_weight, const float* d_bias, float eps, void* d_y,
+                      long long ldy, float* d_stats, cudaStream_t st);
+size_t layer_norm_backward_ws_bytes(int n, int width);
+int launch_layer_norm_backward(const void* d_x, long long ldx, int n, int width, int dtype,
+                               const float* d_weight, const float* d_stats, const void* d_grad,
+                               long long ldg, void* d_ws, void* d_dx, long long lddx,
+                               float* d_dweight, float* d_dbias, cudaStream_t st);
+
 }  // namespace egat

@@ -1,0 +1,704 @@
+// Attention within each molecule, forward and backward, for every shape and
+// storage type on the FMA pipe in float32, and the host side: which kernels a
+// shape takes, key splits, workspaces.
+//
+//   x_ij = q_i.k_j / sqrt(dk),  s_ij = f(x_ij) - slope |r_i - r_j|,
+//   f(x) = x or cap tanh(x / cap),  m_i = sum_j softmax_j(s_ij) h'_j
+//
+// The rows of one head are taken in tiles of one molecule (molecule.cuh); a
+// group of LP lanes holds a row: its query, its accumulators and, backward,
+// its gradient, split over the lanes in float4 vectors.  Key (or, for the
+// gradients of the keys, query) rows pass through shared memory as float32
+// and are read by broadcast, so a warp's read serves 32 / LP rows.  The
+// softmax runs online with base-2 exponents: one running maximum and sum per
+// row, rescaled only when the maximum grows.
+#include <cmath>
+
+#include "molecule.cuh"
+
+namespace egat {
+namespace {
+
+constexpr int kMolThreads = 128;
+constexpr int kMolWarps = kMolThreads / 32;
+constexpr int kMolBatch = 4;   // keys taken together by the online softmax
+
+template <int NV, int LP>
+struct MolRows {
+  static constexpr int KV = LP >= 8 ? 1 : 8 / LP;    // query vectors of a lane (dk <= 32)
+  static constexpr int M = kMolWarps * (32 / LP);    // rows of a tile
+  static constexpr int DV = 4 * NV * LP;             // value columns
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+__device__ __forceinline__ void axpy4(float s, float4 b, float4& c) {
+  c.x = fmaf(s, b.x, c.x);
+  c.y = fmaf(s, b.y, c.y);
+  c.z = fmaf(s, b.z, c.z);
+  c.w = fmaf(s, b.w, c.w);
+}
+__device__ __forceinline__ void scale4(float s, float4& c) {
+  c.x *= s;
+  c.y *= s;
+  c.z *= s;
+  c.w *= s;
+}
+template <int LP>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int o = LP / 2; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// offset of value vector x (4 columns) of a head inside a row of [D][C]
+__device__ __forceinline__ int val_off(const MolParams& p, int head, int x) {
+  const int vlog = p.ch8log + 1;   // vectors of a head's channels: ch / 4
+  return (x >> vlog) * p.C + head * p.ch + ((x & ((1 << vlog) - 1)) << 2);
+}
+
+// A tile of `kb` rows [r0, end) of one head into shared memory as float32:
+// the query/key part, the value part and the positions.  Rows from `end` on
+// are zeros, so nothing of another molecule enters a product.
+template <int DV, typename T>
+__device__ __forceinline__ void stage_rows(const MolParams& p, int head, const T* qk, const T* val,
+                                           const float* pos, int r0, int end, float* sk, float* sv,
+                                           float* sp) {
+  const int kv = p.dk / 4;
+  for (int i = threadIdx.x; i < p.kb * kv; i += kMolThreads) {
+    const int r = i / kv, x = i - r * kv;
+    const bool in = r0 + r < end;
+    const float4 v = in ? load4(qk + (size_t(r0 + r) * p.H + head) * p.dk + 4 * x)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(sk + r * p.dk + 4 * x) = v;
+  }
+  for (int i = threadIdx.x; i < p.kb * (DV / 4); i += kMolThreads) {
+    const int r = i / (DV / 4), x = i - r * (DV / 4);
+    const bool in = r0 + r < end;
+    const float4 v = in ? load4(val + size_t(r0 + r) * p.D * p.C + val_off(p, head, x))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(sv + r * DV + 4 * x) = v;
+  }
+  if (p.a.slope)
+    for (int i = threadIdx.x; i < p.kb; i += kMolThreads) {
+      const bool in = r0 + i < end;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in) {
+        const float* r = pos + size_t(r0 + i) * 3;
+        v = make_float4(r[0], r[1], r[2], 0.f);
+      }
+      *reinterpret_cast<float4*>(sp + 4 * i) = v;
+    }
+}
+
+// ---- forward
+
+template <int NV, int LP, typename T>
+__global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
+  using R = MolRows<NV, LP>;
+  extern __shared__ __align__(16) float msm[];
+  float* sk = msm;
+  float* sv = sk + p.kb * p.dk;
+  float* sp = sv + p.kb * R::DV;
+  const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
+  const MolTile t = mol_tile<R::M>(p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  if (t.rows <= 0) return;
+  const int own = threadIdx.x / LP;
+  const bool live = own < t.rows;
+  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const size_t row = size_t(t.row0) + (live ? own : 0);
+  const int kv = p.dk / 4;
+  float4 q[R::KV];
+#pragma unroll
+  for (int i = 0; i < R::KV; ++i) {
+    const int x = l + LP * i;
+    q[i] = x < kv ? load4(static_cast<const T*>(p.a.q) + (row * p.H + head) * p.dk + 4 * x)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float rx = 0.f, ry = 0.f, rz = 0.f, slope = 0.f;
+  if (p.a.slope) {
+    rx = p.a.posq[row * 3];
+    ry = p.a.posq[row * 3 + 1];
+    rz = p.a.posq[row * 3 + 2];
+    slope = p.a.slope[head] * kLog2e;
+  }
+  float4 o[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float mx = -INFINITY, sum = 0.f;
+  // this split's share of the molecule's key tiles
+  const int tiles = (t.o1 - t.o0 + p.kb - 1) / p.kb, per = (tiles + p.splits - 1) / p.splits;
+  const int k_begin = t.o0 + int(blockIdx.z) * per * p.kb;
+  const int k_end = min(t.o1, k_begin + per * p.kb);
+  for (int k0 = k_begin; k0 < k_end; k0 += p.kb) {
+    __syncthreads();
+    stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
+                         k0, k_end, sk, sv, sp);
+    __syncthreads();
+    if (!warp_live) continue;
+    const int nk = min(p.kb, k_end - k0);
+    for (int j0 = 0; j0 < nk; j0 += kMolBatch) {
+      float s[kMolBatch];
+#pragma unroll
+      for (int b = 0; b < kMolBatch; ++b) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < R::KV; ++i)
+          if (l + LP * i < kv)
+            x = dot4(q[i], *reinterpret_cast<const float4*>(sk + (j0 + b) * p.dk + 4 * (l + LP * i)), x);
+        x = group_sum<LP>(x) * p.scale;
+        float unused;
+        if (p.cap > 0.f) x = p.cap * mol_tanh(x * p.inv_cap, unused);
+        x *= kLog2e;
+        if (p.a.slope) {
+          const float4 r = *reinterpret_cast<const float4*>(sp + 4 * (j0 + b));
+          const float dx = rx - r.x, dy = ry - r.y, dz = rz - r.z;
+          x -= slope * mol_sqrt(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        }
+        s[b] = j0 + b < nk ? x : -INFINITY;
+      }
+      const float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      if (__any_sync(~0u, top > mx)) {
+        const float up = fmaxf(mx, top);
+        const float f = up == -INFINITY ? 1.f : fast_exp2(mx - up);
+        mx = up;
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) scale4(f, o[i]);
+      }
+      const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int b = 0; b < kMolBatch; ++b) {
+        const float w = fast_exp2(s[b] - ref);
+        sum += w;
+        const float* v = sv + (j0 + b) * R::DV + 4 * l;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) axpy4(w, *reinterpret_cast<const float4*>(v + 4 * LP * i), o[i]);
+      }
+    }
+  }
+  if (!live) return;
+  if (p.splits > 1) {
+    const size_t at = (size_t(blockIdx.z) * p.nq + row) * p.H + head;
+    if (l == 0) {
+      p.part_ml[2 * at] = mx;
+      p.part_ml[2 * at + 1] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store4(p.part_o + at * p.dv + 4 * (l + LP * i), o[i]);
+    return;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (l == 0 && p.lse) p.lse[row * p.H + head] = sum == 0.f ? -INFINITY : mx * kLn2 + logf(sum);
+  T* out = static_cast<T*>(p.m) + row * p.D * p.C;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    scale4(inv, o[i]);
+    store4(out + val_off(p, head, l + LP * i), o[i]);
+  }
+}
+
+// Joins the key splits: one warp per row and head.
+template <typename T>
+__global__ void mol_join_kernel(MolParams p) {
+  const int lane = threadIdx.x & 31;
+  const size_t rh = (size_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
+  const size_t total = size_t(p.nq) * p.H;
+  if (rh >= total) return;
+  const size_t row = rh / p.H;
+  const int head = int(rh - row * p.H);
+  float mx = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[2 * (s * total + rh)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  for (int s = lane; s < p.splits; s += 32) {
+    const float* ml = p.part_ml + 2 * (s * total + rh);
+    sum += ml[1] * fast_exp2(ml[0] - ref);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (lane == 0 && p.lse) p.lse[rh] = sum == 0.f ? -INFINITY : mx * kLn2 + logf(sum);
+  T* out = static_cast<T*>(p.m) + row * p.D * p.C;
+  for (int x = lane; x < p.dv / 4; x += 32) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.splits; ++s) {
+      const float w = fast_exp2(p.part_ml[2 * (s * total + rh)] - ref);
+      axpy4(w, *reinterpret_cast<const float4*>(p.part_o + (s * total + rh) * p.dv + 4 * x), acc);
+    }
+    scale4(inv, acc);
+    store4(out + val_off(p, head, x), acc);
+  }
+}
+
+// ---- backward
+
+// The softmax weight and the score's derivative dx of one pair: x = q.k (not
+// yet scaled), d = distance, lse2 = the row's log-sum-exp in base 2.
+__device__ __forceinline__ float pair_weight(const MolParams& p, float x, float bias2, float lse2,
+                                             float& slope_x) {
+  x *= p.scale;
+  slope_x = p.scale;
+  if (p.cap > 0.f) {
+    float d;
+    x = p.cap * mol_tanh(x * p.inv_cap, d);
+    slope_x *= d;
+  }
+  return lse2 == -INFINITY ? 0.f : fast_exp2(fmaf(x, kLog2e, -bias2) - lse2);
+}
+
+// dL/dq, the row sums delta, and the query side of dL/dr and dL/dslope.
+template <int NV, int LP, typename T>
+__global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
+  using R = MolRows<NV, LP>;
+  extern __shared__ __align__(16) float msm[];
+  float* sk = msm;
+  float* sv = sk + p.kb * p.dk;
+  float* sp = sv + p.kb * R::DV;
+  __shared__ float warp_ds[kMolWarps];
+  const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
+  const MolTile t = mol_tile<R::M>(p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  if (t.rows <= 0) {
+    if (p.want_pos && threadIdx.x == 0) p.part_ds[size_t(head) * p.slots + blockIdx.x] = 0.f;
+    return;
+  }
+  const int own = threadIdx.x / LP;
+  const bool live = own < t.rows;
+  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const size_t row = size_t(t.row0) + (live ? own : 0);
+  const int kv = p.dk / 4;
+  float4 q[R::KV], dq[R::KV], g[NV];
+  float delta = 0.f;
+#pragma unroll
+  for (int i = 0; i < R::KV; ++i) {
+    const int x = l + LP * i;
+    q[i] = x < kv ? load4(static_cast<const T*>(p.a.q) + (row * p.H + head) * p.dk + 4 * x)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    dq[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const size_t at = row * p.D * p.C + val_off(p, head, l + LP * i);
+    g[i] = load4(static_cast<const T*>(p.g.g) + at);
+    if (!p.exact_delta) delta = dot4(g[i], load4(static_cast<const T*>(p.g.m) + at), delta);
+  }
+  delta = group_sum<LP>(delta);
+  const float lse2 = p.g.lse[row * p.H + head] * kLog2e;
+  float rx = 0.f, ry = 0.f, rz = 0.f, slope = 0.f;
+  if (p.a.slope) {
+    rx = p.a.posq[row * 3];
+    ry = p.a.posq[row * 3 + 1];
+    rz = p.a.posq[row * 3 + 2];
+    slope = p.a.slope[head];
+  }
+  float gx = 0.f, gy = 0.f, gz = 0.f, ds_sum = 0.f;
+  for (int sweep = p.exact_delta ? 0 : 1; sweep < 2; ++sweep) {
+    for (int k0 = t.o0; k0 < t.o1; k0 += p.kb) {
+      __syncthreads();
+      stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
+                           k0, t.o1, sk, sv, sp);
+      __syncthreads();
+      if (!warp_live) continue;
+      const int nk = min(p.kb, t.o1 - k0);
+      for (int j = 0; j < nk; ++j) {
+        float x = 0.f, dp = 0.f;
+#pragma unroll
+        for (int i = 0; i < R::KV; ++i)
+          if (l + LP * i < kv)
+            x = dot4(q[i], *reinterpret_cast<const float4*>(sk + j * p.dk + 4 * (l + LP * i)), x);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          dp = dot4(g[i], *reinterpret_cast<const float4*>(sv + j * R::DV + 4 * (l + LP * i)), dp);
+        x = group_sum<LP>(x);
+        dp = group_sum<LP>(dp);
+        float d = 0.f, dx = 0.f, dy = 0.f, dz = 0.f, slope_x;
+        if (p.a.slope) {
+          const float4 r = *reinterpret_cast<const float4*>(sp + 4 * j);
+          dx = rx - r.x, dy = ry - r.y, dz = rz - r.z;
+          d = mol_sqrt(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        }
+        const float w = pair_weight(p, x, slope * kLog2e * d, lse2, slope_x);
+        if (sweep == 0) {
+          delta = fmaf(w, dp, delta);
+          continue;
+        }
+        const float ds = w * (dp - delta);
+        if (p.want_pos) {
+          ds_sum -= ds != 0.f ? ds * d : 0.f;   // d may be inf where the weight is 0
+          const float u = d > 0.f ? __fdividef(-slope * ds, d) : 0.f;
+          gx = fmaf(u, dx, gx);
+          gy = fmaf(u, dy, gy);
+          gz = fmaf(u, dz, gz);
+        }
+#pragma unroll
+        for (int i = 0; i < R::KV; ++i)
+          if (l + LP * i < kv)
+            axpy4(ds * slope_x, *reinterpret_cast<const float4*>(sk + j * p.dk + 4 * (l + LP * i)), dq[i]);
+      }
+    }
+  }
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < R::KV; ++i)
+      if (l + LP * i < kv)
+        store4(static_cast<T*>(p.g.dq) + (row * p.H + head) * p.dk + 4 * (l + LP * i), dq[i]);
+    if (l == 0) {
+      p.delta[row * p.H + head] = delta;
+      if (p.want_pos) {
+        float* at = p.part_dq + (size_t(head) * p.nq + row) * 3;
+        at[0] = gx;
+        at[1] = gy;
+        at[2] = gz;
+      }
+    }
+  }
+  if (p.want_pos) {
+    float v = live && l == 0 ? ds_sum : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if (lane == 0) warp_ds[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float sum = 0.f;
+      for (int i = 0; i < kMolWarps; ++i) sum += warp_ds[i];
+      p.part_ds[size_t(head) * p.slots + blockIdx.x] = sum;
+    }
+  }
+}
+
+// dL/dk, dL/dh' and the key side of dL/dr: a lane group owns a key row and
+// meets the molecule's query rows.
+template <int NV, int LP, typename T>
+__global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
+  using R = MolRows<NV, LP>;
+  extern __shared__ __align__(16) float msm[];
+  float* sq = msm;
+  float* sg = sq + p.kb * p.dk;
+  float* sp = sg + p.kb * R::DV;
+  float* sl = sp + 4 * p.kb;   // lse2, delta
+  const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
+  const MolTile t = mol_tile<R::M>(p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
+  if (t.rows <= 0) return;
+  const int own = threadIdx.x / LP;
+  const bool live = own < t.rows;
+  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const size_t row = size_t(t.row0) + (live ? own : 0);
+  const int kv = p.dk / 4;
+  float4 k[R::KV], dk[R::KV], v[NV], dv[NV];
+#pragma unroll
+  for (int i = 0; i < R::KV; ++i) {
+    const int x = l + LP * i;
+    k[i] = x < kv ? load4(static_cast<const T*>(p.a.k) + (row * p.H + head) * p.dk + 4 * x)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    dk[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = load4(static_cast<const T*>(p.a.hp) + row * p.D * p.C + val_off(p, head, l + LP * i));
+    dv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float rx = 0.f, ry = 0.f, rz = 0.f, slope = 0.f;
+  if (p.a.slope) {
+    rx = p.a.posk[row * 3];
+    ry = p.a.posk[row * 3 + 1];
+    rz = p.a.posk[row * 3 + 2];
+    slope = p.a.slope[head];
+  }
+  float gx = 0.f, gy = 0.f, gz = 0.f;
+  for (int q0 = t.o0; q0 < t.o1; q0 += p.kb) {
+    __syncthreads();
+    stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.q), static_cast<const T*>(p.g.g), p.a.posq, q0,
+                         t.o1, sq, sg, sp);
+    for (int i = threadIdx.x; i < p.kb; i += kMolThreads) {
+      const bool in = q0 + i < t.o1;
+      const size_t at = size_t(q0 + i) * p.H + head;
+      sl[2 * i] = in ? p.g.lse[at] * kLog2e : -INFINITY;
+      sl[2 * i + 1] = in ? p.delta[at] : 0.f;
+    }
+    __syncthreads();
+    if (!warp_live) continue;
+    const int nq = min(p.kb, t.o1 - q0);
+    for (int j = 0; j < nq; ++j) {
+      float x = 0.f, dp = 0.f;
+#pragma unroll
+      for (int i = 0; i < R::KV; ++i)
+        if (l + LP * i < kv)
+          x = dot4(k[i], *reinterpret_cast<const float4*>(sq + j * p.dk + 4 * (l + LP * i)), x);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        dp = dot4(v[i], *reinterpret_cast<const float4*>(sg + j * R::DV + 4 * (l + LP * i)), dp);
+      x = group_sum<LP>(x);
+      dp = group_sum<LP>(dp);
+      float d = 0.f, dx = 0.f, dy = 0.f, dz = 0.f, slope_x;
+      if (p.a.slope) {
+        const float4 r = *reinterpret_cast<const float4*>(sp + 4 * j);
+        dx = rx - r.x, dy = ry - r.y, dz = rz - r.z;
+        d = mol_sqrt(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+      }
+      const float w = pair_weight(p, x, slope * kLog2e * d, sl[2 * j], slope_x);
+      const float ds = w * (dp - sl[2 * j + 1]);
+      if (p.want_pos) {
+        const float u = d > 0.f ? __fdividef(-slope * ds, d) : 0.f;
+        gx = fmaf(u, dx, gx);
+        gy = fmaf(u, dy, gy);
+        gz = fmaf(u, dz, gz);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        axpy4(w, *reinterpret_cast<const float4*>(sg + j * R::DV + 4 * (l + LP * i)), dv[i]);
+#pragma unroll
+      for (int i = 0; i < R::KV; ++i)
+        if (l + LP * i < kv)
+          axpy4(ds * slope_x, *reinterpret_cast<const float4*>(sq + j * p.dk + 4 * (l + LP * i)), dk[i]);
+    }
+  }
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < R::KV; ++i)
+    if (l + LP * i < kv)
+      store4(static_cast<T*>(p.g.dk) + (row * p.H + head) * p.dk + 4 * (l + LP * i), dk[i]);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    store4(static_cast<T*>(p.g.dhp) + row * p.D * p.C + val_off(p, head, l + LP * i), dv[i]);
+  if (p.want_pos && l == 0) {
+    float* at = p.part_dk + (size_t(head) * p.nk + row) * 3;
+    at[0] = gx;
+    at[1] = gy;
+    at[2] = gz;
+  }
+}
+
+// dL/dr summed over heads (and, in the self form, over both roles of an
+// atom); the last H blocks sum dL/dslope over query tiles, in a fixed order.
+__global__ void mol_reduce_kernel(MolParams p, int pos_blocks) {
+  if (int(blockIdx.x) < pos_blocks) {
+    const long long nq3 = 3LL * p.nq, nk3 = 3LL * p.nk;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long j = p.a.self ? i : i - nq3;
+    if (i < nq3 && p.g.dposq) {
+      float s = 0.f;
+      for (int h = 0; h < p.H; ++h) {
+        s += p.part_dq[h * nq3 + i];
+        if (p.a.self) s += p.part_dk[h * nk3 + i];
+      }
+      p.g.dposq[i] = s;
+    }
+    if (!p.a.self && j >= 0 && j < nk3 && p.g.dposk) {
+      float s = 0.f;
+      for (int h = 0; h < p.H; ++h) s += p.part_dk[h * nk3 + j];
+      p.g.dposk[j] = s;
+    }
+    return;
+  }
+  if (!p.g.dslope) return;
+  __shared__ float part[256];
+  const int h = blockIdx.x - pos_blocks;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < p.slots; i += 256) s += p.part_ds[size_t(h) * p.slots + i];
+  part[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if (int(threadIdx.x) < o) part[threadIdx.x] += part[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.g.dslope[h] = part[0];
+}
+
+// Value columns of a head as NV float4 vectors in each of LP lanes: dv / 4 is
+// a power of two, or nine times one at lmax 2.  Up to nine vectors a lane
+// keep the accumulators of a row in registers.
+template <typename F>
+int by_rows(int dv, F&& f) {
+  switch (dv / 4) {
+#define EGAT_ROWS(n, NV, LP) \
+  case n: return f(std::integral_constant<int, NV>{}, std::integral_constant<int, LP>{})
+    EGAT_ROWS(2, 2, 1);
+    EGAT_ROWS(4, 4, 1);
+    EGAT_ROWS(8, 8, 1);
+    EGAT_ROWS(16, 8, 2);
+    EGAT_ROWS(32, 8, 4);
+    EGAT_ROWS(64, 8, 8);
+    EGAT_ROWS(128, 8, 16);
+    EGAT_ROWS(256, 8, 32);
+    EGAT_ROWS(512, 16, 32);
+    EGAT_ROWS(18, 9, 2);
+    EGAT_ROWS(36, 9, 4);
+    EGAT_ROWS(72, 9, 8);
+    EGAT_ROWS(144, 9, 16);
+    EGAT_ROWS(288, 9, 32);
+#undef EGAT_ROWS
+    default: return EGAT_ERR_UNSUPPORTED;
+  }
+}
+
+size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+int ceil_log2(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+int head_columns(const egat_mol_shape& s) { return (s.lmax + 1) * (s.lmax + 1) * (s.C / s.H); }
+// rows of a generic tile, and a lower bound of it for workspace sizes
+int generic_rows(const egat_mol_shape& s) {
+  int m = 4;
+  by_rows(head_columns(s), [&](auto nv, auto lp) {
+    m = MolRows<decltype(nv)::value, decltype(lp)::value>::M;
+    return 0;
+  });
+  return m;
+}
+
+// Key splits: with fewer row tiles than four waves of 148 SMs, each
+// molecule's keys are cut so that about that many blocks run, but not below
+// 128 keys a part on average.  Depends on the shape alone.
+int key_splits(const egat_mol_shape& s, int tile_rows) {
+  if (s.n_mol == 0 || s.nk == 0) return 1;
+  const long long blocks = ((long long)s.nq / tile_rows + std::min(s.n_mol, s.nq) + 1) * s.H;
+  const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
+  return int(std::max(1LL, std::min(std::min(most, want), 64LL)));
+}
+
+MolParams base_params(const egat_mol_shape& s, const MolArgs& a) {
+  MolParams p{};
+  p.a = a;
+  p.nq = s.nq;
+  p.nk = s.nk;
+  p.nmol = s.n_mol;
+  p.D = (s.lmax + 1) * (s.lmax + 1);
+  p.C = s.C;
+  p.H = s.H;
+  p.dk = s.dk;
+  p.ch = s.C / s.H;
+  p.ch8log = ceil_log2(p.ch / 8);
+  p.dv = p.D * p.ch;
+  p.splits = 1;
+  p.scale = 1.f / std::sqrt(float(s.dk));
+  p.cap = s.cap;
+  p.inv_cap = s.cap > 0.f ? 1.f / s.cap : 0.f;
+  // rows of a staged tile: up to 32 within 40 KB
+  p.kb = std::max(kMolBatch, std::min(32, int(40 * 1024 / (4 * (s.dk + p.dv + 6))) & ~(kMolBatch - 1)));
+  return p;
+}
+size_t stage_bytes(const MolParams& p) { return size_t(p.kb) * (p.dk + p.dv + 6) * sizeof(float); }
+int launched() { return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA; }
+
+template <typename T>
+int forward_t(MolParams p, cudaStream_t st) {
+  const int rc = by_rows(p.dv, [&](auto nv, auto lp) {
+    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value;
+    p.slots = mol_slots(p.nq, p.nmol, MolRows<NV, LP>::M);
+    mol_fwd_kernel<NV, LP, T><<<dim3(p.slots, p.H, p.splits), kMolThreads, stage_bytes(p), st>>>(p);
+    return launched();
+  });
+  if (rc != EGAT_OK || p.splits == 1) return rc;
+  const size_t warps = size_t(p.nq) * p.H;
+  mol_join_kernel<T><<<unsigned((warps + 3) / 4), 128, 0, st>>>(p);
+  return launched();
+}
+
+template <typename T>
+int backward_t(MolParams p, cudaStream_t st) {
+  return by_rows(p.dv, [&](auto nv, auto lp) {
+    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value, M = MolRows<NV, LP>::M;
+    p.slots = mol_slots(p.nq, p.nmol, M);
+    if (p.nq > 0) {
+      mol_bwd_q_kernel<NV, LP, T><<<dim3(p.slots, p.H), kMolThreads, stage_bytes(p), st>>>(p);
+      if (launched() != EGAT_OK) return int(EGAT_ERR_CUDA);
+    }
+    if (p.nk > 0) {
+      const int ks = mol_slots(p.nk, p.nmol, M);
+      mol_bwd_k_kernel<NV, LP, T><<<dim3(ks, p.H), kMolThreads, stage_bytes(p), st>>>(p);
+      if (launched() != EGAT_OK) return int(EGAT_ERR_CUDA);
+    }
+    return int(EGAT_OK);
+  });
+}
+
+// Workspace of the backward pass: delta, then the partial sums of the
+// position and slope gradients.
+struct MolBwdWs {
+  size_t delta, dq, dk, ds, total;
+};
+MolBwdWs bwd_ws(const egat_mol_shape& s, int slots) {
+  MolBwdWs w;
+  w.delta = 0;
+  w.dq = up256(sizeof(float) * size_t(s.nq) * s.H);
+  w.dk = w.dq + up256(sizeof(float) * 3 * size_t(s.nq) * s.H);
+  w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * s.H);
+  w.total = w.ds + up256(sizeof(float) * size_t(slots) * s.H);
+  return w;
+}
+
+}  // namespace
+
+size_t molecule_ws_bytes(const egat_mol_shape& s) {
+  const int splits = key_splits(s, generic_rows(s));
+  if (splits == 1) return 0;
+  const size_t rows = size_t(splits) * s.nq * s.H;
+  return up256(rows * head_columns(s) * sizeof(float)) + up256(rows * 2 * sizeof(float));
+}
+
+int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d_ws, void* d_m,
+                              float* d_lse, cudaStream_t st) {
+  MolParams p = base_params(s, a);
+  p.m = d_m;
+  p.lse = d_lse;
+  p.splits = key_splits(s, generic_rows(s));
+  if (p.splits > 1) {
+    p.part_o = static_cast<float*>(d_ws);
+    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(d_ws) +
+                                         up256(size_t(p.splits) * s.nq * s.H * p.dv * sizeof(float)));
+  }
+  return s.dtype == EGAT_BF16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
+}
+
+size_t molecule_backward_ws_bytes(const egat_mol_shape& s) {
+  return bwd_ws(s, mol_slots(s.nq, s.n_mol, generic_rows(s))).total;
+}
+
+int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const MolGrads& g,
+                             void* d_ws, cudaStream_t st) {
+  MolParams p = base_params(s, a);
+  p.g = g;
+  const int slots = mol_slots(s.nq, s.n_mol, generic_rows(s));
+  const MolBwdWs w = bwd_ws(s, slots);
+  char* base = static_cast<char*>(d_ws);
+  p.delta = reinterpret_cast<float*>(base + w.delta);
+  p.part_dq = reinterpret_cast<float*>(base + w.dq);
+  p.part_dk = reinterpret_cast<float*>(base + w.dk);
+  p.part_ds = reinterpret_cast<float*>(base + w.ds);
+  p.want_pos = g.dposq || g.dposk || g.dslope;
+  // float32 m gives delta to float32; bf16 m would leave it bf16's error, which
+  // showed as 1.6 times the rounding error of dq (4,096 atoms, 16 heads)
+  p.exact_delta = s.dtype == EGAT_BF16;
+  p.slots = slots;
+  const int rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, st) : backward_t<float>(p, st);
+  if (rc != EGAT_OK || !p.want_pos) return rc;
+  if (s.nq == 0) {   // no query tile ran
+    if (g.dslope && cudaMemsetAsync(g.dslope, 0, sizeof(float) * s.H, st) != cudaSuccess)
+      return EGAT_ERR_CUDA;
+    if (!g.dposk) return EGAT_OK;
+    p.g.dslope = nullptr;
+  }
+  const long long rows3 = 3LL * s.nq + (a.self ? 0 : 3LL * s.nk);
+  const int pos_blocks = int((rows3 + 255) / 256);
+  mol_reduce_kernel<<<pos_blocks + s.H, 256, 0, st>>>(p, pos_blocks);
+  return launched();
+}
+
+}  // namespace egat

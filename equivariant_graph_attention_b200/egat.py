@@ -42,7 +42,11 @@ EXPORTS = ["egat_version", "egat_strerror", "egat_num_paths", "egat_graph_worksp
            "egat_attention_plan_bytes", "egat_build_attention_plan", "egat_otf_attention_tiled",
            "egat_eaas_couple_planned", "egat_take_device_status", "egat_selftest_wait_timeout",
            "egat_backward_workspace_bytes", "egat_backward", "egat_gather_rows",
-           "egat_qk_projection", "egat_escn_num_weights", "egat_escn_conv"]
+           "egat_qk_projection", "egat_escn_num_weights", "egat_escn_conv",
+           "egat_molecule_attention_workspace_bytes", "egat_molecule_attention",
+           "egat_molecule_attention_backward_workspace_bytes", "egat_molecule_attention_backward",
+           "egat_layer_norm", "egat_layer_norm_backward_workspace_bytes",
+           "egat_layer_norm_backward"]
 
 
 class EgatError(RuntimeError):
@@ -56,6 +60,12 @@ class egat_shape(ctypes.Structure):
                 ("H", ctypes.c_int32), ("dk", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("graph_mode", ctypes.c_int32),
                 ("n_edges", ctypes.c_int64)]
+
+
+class egat_mol_shape(ctypes.Structure):
+    _fields_ = [("nq", ctypes.c_int32), ("nk", ctypes.c_int32), ("n_mol", ctypes.c_int32),
+                ("lmax", ctypes.c_int32), ("C", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dtype", ctypes.c_int32), ("cap", ctypes.c_float)]
 
 
 _lib = None
@@ -119,6 +129,22 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.egat_otf_attention_tiled.argtypes = [sp, vp, vp, vp, vp, vp, vp, i32, vp]
     lib.egat_forward_noalloc.restype = ctypes.c_int
     lib.egat_forward_noalloc.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    mp, f32 = ctypes.POINTER(egat_mol_shape), ctypes.c_float
+    for name in ("egat_molecule_attention_workspace_bytes",
+                 "egat_molecule_attention_backward_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = [mp, ctypes.POINTER(sz)]
+    lib.egat_molecule_attention.restype = ctypes.c_int
+    lib.egat_molecule_attention.argtypes = [mp] + [vp] * 9 + [sz, vp, vp, vp]
+    lib.egat_molecule_attention_backward.restype = ctypes.c_int
+    lib.egat_molecule_attention_backward.argtypes = [mp] + [vp] * 12 + [sz] + [vp] * 7
+    lib.egat_layer_norm.restype = ctypes.c_int
+    lib.egat_layer_norm.argtypes = [vp, i64, i32, i32, i32, vp, vp, f32, vp, i64, vp, vp]
+    lib.egat_layer_norm_backward_workspace_bytes.restype = ctypes.c_int
+    lib.egat_layer_norm_backward_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
+    lib.egat_layer_norm_backward.restype = ctypes.c_int
+    lib.egat_layer_norm_backward.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, i64, vp, sz, vp,
+                                             i64, vp, vp, vp]
     if path is None:
         _lib = lib
     return lib
@@ -474,3 +500,210 @@ def egat_forward_noalloc(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: to
         _ptr(cnt_or_col), _ptr(order), _ptr(w1), _ptr(w2), _ptr(out), _stream(stream))
     _check("egat_forward_noalloc", rc)
     return out
+
+
+@dataclass(frozen=True)
+class MoleculeShape:
+    """Shape of the attention within each molecule: nq query rows and nk key
+    rows in n_mol molecules; cap = tanh cap of the scores (0: none)."""
+    nq: int
+    nk: int
+    n_mol: int
+    lmax: int
+    C: int
+    H: int
+    dk: int
+    dtype: str = "f32"          # "f32" or "bf16": storage of every feature and gradient
+    cap: float = 0.0
+
+    @property
+    def D(self) -> int:
+        return (self.lmax + 1) ** 2
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+    def c(self) -> egat_mol_shape:
+        return egat_mol_shape(self.nq, self.nk, self.n_mol, self.lmax, self.C, self.H, self.dk,
+                              EGAT_BF16 if self.dtype == "bf16" else EGAT_F32, self.cap)
+
+
+def _typed(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Optional[int]:
+    """The pointer of a contiguous tensor of this type, shape and device; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"egat: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"egat: {name} is on {t.device}, not on {device}")
+    return _ptr(t)
+
+
+def _scratch(nb: int, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(nb, 16), dtype=torch.uint8, device=device)
+    if workspace.device != device:
+        raise ValueError(f"egat: workspace is on {workspace.device}, not on {device}")
+    return workspace
+
+
+def _mol_inputs(s: MoleculeShape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev):
+    T = s.torch_dtype
+    return [_typed("q", q, T, (s.nq, s.H, s.dk), dev), _typed("k", k, T, (s.nk, s.H, s.dk), dev),
+            _typed("hp", hp, T, (s.nk, s.D, s.C), dev),
+            _typed("q_ptr", q_ptr, torch.int32, (s.n_mol + 1,), dev),
+            _typed("k_ptr", k_ptr, torch.int32, (s.n_mol + 1,), dev),
+            _typed("pos_q", pos_q, torch.float32, (s.nq, 3), dev),
+            _typed("pos_k", pos_k, torch.float32, (s.nk, 3), dev),
+            _typed("slope", slope, torch.float32, (s.H,), dev)]
+
+
+def egat_molecule_attention_workspace_bytes(shape: MoleculeShape) -> int:
+    out = ctypes.c_size_t(0)
+    cs = shape.c()
+    _check("egat_molecule_attention_workspace_bytes",
+           load_library().egat_molecule_attention_workspace_bytes(ctypes.byref(cs), ctypes.byref(out)))
+    return out.value
+
+
+def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tensor,
+                            hp: torch.Tensor, q_ptr: torch.Tensor,
+                            k_ptr: Optional[torch.Tensor] = None,
+                            pos_q: Optional[torch.Tensor] = None,
+                            pos_k: Optional[torch.Tensor] = None,
+                            slope: Optional[torch.Tensor] = None, want_lse: bool = False,
+                            out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None):
+    """All-pairs attention within each molecule, scores q_i.k_j / sqrt(dk), capped by
+    cap tanh(. / cap) when shape.cap > 0, minus slope_h |r_i - r_j| when slope is given.
+
+    Molecule b: query rows q_ptr[b]:q_ptr[b+1], key rows k_ptr[b]:k_ptr[b+1] (int32 on the
+    device; k_ptr None: the queries' own atoms).  Returns (m [nq, D, C] in the storage type,
+    lse float32 [nq, H] or None); rows without keys get 0 and -inf."""
+    dev = q.device
+    with torch.cuda.device(dev):
+        ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+        if out is None:
+            out = torch.empty((shape.nq, shape.D, shape.C), dtype=shape.torch_dtype, device=dev)
+        po = _typed("out", out, shape.torch_dtype, (shape.nq, shape.D, shape.C), dev)
+        lse = torch.empty((shape.nq, shape.H), dtype=torch.float32, device=dev) if want_lse else None
+        ws = _scratch(egat_molecule_attention_workspace_bytes(shape), workspace, dev)
+        cs = shape.c()
+        rc = load_library().egat_molecule_attention(ctypes.byref(cs), *ptrs, _ptr(ws), ws.numel(), po,
+                                                    _ptr(lse), _stream(stream))
+    _check("egat_molecule_attention", rc)
+    return out, lse
+
+
+def egat_molecule_attention_backward_workspace_bytes(shape: MoleculeShape) -> int:
+    out = ctypes.c_size_t(0)
+    cs = shape.c()
+    _check("egat_molecule_attention_backward_workspace_bytes",
+           load_library().egat_molecule_attention_backward_workspace_bytes(ctypes.byref(cs),
+                                                                           ctypes.byref(out)))
+    return out.value
+
+
+def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: torch.Tensor,
+                                     hp: torch.Tensor, q_ptr: torch.Tensor, m: torch.Tensor,
+                                     lse: torch.Tensor, grad_m: torch.Tensor,
+                                     k_ptr: Optional[torch.Tensor] = None,
+                                     pos_q: Optional[torch.Tensor] = None,
+                                     pos_k: Optional[torch.Tensor] = None,
+                                     slope: Optional[torch.Tensor] = None, positions: bool = True,
+                                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of <grad_m, m> for the forward's m and lse: (dq, dk, dhp) in the storage
+    type and (dpos_q, dpos_k, dslope) float32.  In the self form (k_ptr None) dpos_q is the
+    whole dL/dr and dpos_k is None; without a slope, or with positions=False (cheaper), the
+    last three are None."""
+    dev, T = q.device, shape.torch_dtype
+    with torch.cuda.device(dev):
+        ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+        vals = (shape.nq, shape.D, shape.C)
+        ptrs += [_typed("m", m, T, vals, dev), _typed("lse", lse, torch.float32, (shape.nq, shape.H), dev),
+                 _typed("grad_m", grad_m, T, vals, dev)]
+        ws = _scratch(egat_molecule_attention_backward_workspace_bytes(shape), workspace, dev)
+        dq, dk, dhp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(hp)
+        dpos_q = dpos_k = dslope = None
+        if slope is not None and positions:
+            dpos_q, dslope = torch.empty_like(pos_q), torch.empty_like(slope)
+            dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
+        cs = shape.c()
+        rc = load_library().egat_molecule_attention_backward(
+            ctypes.byref(cs), *ptrs, _ptr(ws), ws.numel(), _ptr(dq), _ptr(dk), _ptr(dhp), _ptr(dpos_q),
+            _ptr(dpos_k), _ptr(dslope), _stream(stream))
+    _check("egat_molecule_attention_backward", rc)
+    return dq, dk, dhp, dpos_q, dpos_k, dslope
+
+
+def _norm_rows(name: str, t: torch.Tensor, dtype, n: int, width: int, device):
+    """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype != dtype or tuple(t.shape) != (n, width):
+        raise ValueError(f"egat: {name} must be {dtype} [{n}, {width}], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"egat: {name} must live on the CUDA device {device}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"egat: {name} must have contiguous rows")
+    ld = t.stride(0) if n > 1 else width
+    if ld < width:
+        raise ValueError(f"egat: rows of {name} overlap")
+    return t.data_ptr() if n > 0 else None, ld
+
+
+def _norm_dtype(x: torch.Tensor) -> int:
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("egat: x must be a float32 or bfloat16 matrix [n, width]")
+    return EGAT_BF16 if x.dtype == torch.bfloat16 else EGAT_F32
+
+
+def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, eps: float = 1e-5, want_stats: bool = False,
+                    out: Optional[torch.Tensor] = None, stream=None):
+    """Layer norm of the rows of x [n, width] (float32 or bf16; any row stride, so h[:, 0, :]
+    works in place), weight and bias float32 [width].  Returns (y, stats float32 [n, 2] = mean
+    and 1/std, or None).  out may be x itself."""
+    dt, (n, width), dev = _norm_dtype(x), x.shape, x.device
+    with torch.cuda.device(dev):
+        px, ldx = _norm_rows("x", x, x.dtype, n, width, dev)
+        pw = _typed("weight", weight, torch.float32, (width,), dev)
+        pb = _typed("bias", bias, torch.float32, (width,), dev)
+        if out is None:
+            out = torch.empty((n, width), dtype=x.dtype, device=dev)
+        py, ldy = _norm_rows("out", out, x.dtype, n, width, dev)
+        stats = torch.empty((n, 2), dtype=torch.float32, device=dev) if want_stats else None
+        rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy, _ptr(stats),
+                                            _stream(stream))
+    _check("egat_layer_norm", rc)
+    return out, stats
+
+
+def egat_layer_norm_backward_workspace_bytes(n: int, width: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("egat_layer_norm_backward_workspace_bytes",
+           load_library().egat_layer_norm_backward_workspace_bytes(n, width, ctypes.byref(out)))
+    return out.value
+
+
+def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], stats: torch.Tensor,
+                             grad_y: torch.Tensor, out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dx in x's type, dweight, dbias float32 [width]) of the layer norm for the upstream
+    gradient grad_y; stats as returned by the forward.  out (any row stride) receives dx."""
+    dt, (n, width), dev = _norm_dtype(x), x.shape, x.device
+    with torch.cuda.device(dev):
+        px, ldx = _norm_rows("x", x, x.dtype, n, width, dev)
+        pg, ldg = _norm_rows("grad_y", grad_y, x.dtype, n, width, dev)
+        pw = _typed("weight", weight, torch.float32, (width,), dev)
+        ps = _typed("stats", stats, torch.float32, (n, 2), dev)
+        if out is None:
+            out = torch.empty((n, width), dtype=x.dtype, device=dev)
+        po, ldo = _norm_rows("out", out, x.dtype, n, width, dev)
+        dw = torch.empty(width, dtype=torch.float32, device=dev)
+        db = torch.empty(width, dtype=torch.float32, device=dev)
+        ws = _scratch(egat_layer_norm_backward_workspace_bytes(n, width), workspace, dev)
+        rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg, _ptr(ws),
+                                                     ws.numel(), po, ldo, _ptr(dw), _ptr(db),
+                                                     _stream(stream))
+    _check("egat_layer_norm_backward", rc)
+    return out, dw, db

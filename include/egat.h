@@ -384,6 +384,122 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
                             const float* d_w, float* d_out, void* stream);
 
 /*
+ * Attention within each molecule of a batch: all pairs, scores optionally
+ * capped by a tanh and biased by distance.  It is the dense counterpart of
+ * step 3 (the pages' roadmap names a hybrid of sparse and dense attention):
+ * the same q, k and h' rows, but a row attends to every key row of its own
+ * molecule (itself included) instead of a neighbour list.
+ *   x_ij = q_i^h . k_j^h / sqrt(dk),  f(x) = x, or cap tanh(x / cap) for cap > 0
+ *   s_ij = f(x_ij) - slope_h |r_i - r_j|
+ *   m_i  = sum_j softmax_j(s_ij)^{head(c)} h'_j,  lse_i^h = log sum_j exp(s_ij)
+ * streamed with an online softmax; nothing of size pairs is written.
+ *
+ * Molecules are runs of consecutive rows: molecule b holds query rows
+ * d_q_ptr[b] .. d_q_ptr[b+1]-1 and attends to key rows d_k_ptr[b] ..
+ * d_k_ptr[b+1]-1 (device arrays of n_mol + 1 ascending entries; entries are
+ * clamped to [0, nq] and [0, nk], so none makes the kernels leave the
+ * buffers).  Lengths are read on the device: no host copy, any length from
+ * zero on.  d_k_ptr = NULL is the self form: nk = nq, keys are the queries'
+ * own atoms and d_pos_k must be NULL.  With d_k_ptr, a few query rows (probe
+ * atoms) attend to long systems; the keys are then split over the GPU and
+ * joined.  A row of no molecule (before the first or behind the last) and a
+ * row whose molecule has no keys get m = 0 and lse = -inf; rows of other
+ * molecules never reach a row's result, not even as NaN.
+ *  s->lmax  0..3 (0: plain scalar values), C, H, dk as in the module header;
+ *           lmax, C and H split the values by head as in step 3
+ *  s->cap   0 = no cap; from 1e-30 to 3e38 otherwise
+ *  d_q [nq][H][dk], d_k [nk][H][dk], d_hp [nk][D][C] in s->dtype
+ *  d_pos_q, d_pos_k float32 [nq][3], [nk][3]; d_slope float32 [H], any sign:
+ *           all used if d_slope is not NULL, none otherwise
+ *  d_m      [nq][D][C] in s->dtype (bf16 storage: the softmax weights enter
+ *           the value products as bf16, so a wider result would not hold more)
+ *  d_lse    float32 [nq][H], natural logarithm; may be NULL (the backward
+ *           pass needs it)
+ *  d_ws     at least egat_molecule_attention_workspace_bytes(s)
+ *  limits   nq and nk up to 2^30, n_mol up to 2^28
+ * Feature and workspace pointers are 16-byte aligned.  Sums and softmax
+ * statistics are float32.  Deterministic.  nq = 0 is a no-op.
+ *
+ * egat_molecule_attention_backward: for an upstream gradient G = dL/dm
+ * ([nq][D][C] in s->dtype, 16-byte aligned) and the forward's m and lse,
+ *  d_dq, d_dk, d_dhp  dL/dq, dL/dk, dL/dh' in s->dtype
+ *  d_dpos_q  float32 [nq][3] dL/dr of the query atoms; in the self form the
+ *            whole dL/dr (as queries and as keys).  May be NULL
+ *  d_dpos_k  float32 [nk][3], with d_k_ptr only.  May be NULL
+ *  d_dslope  float32 [H].  May be NULL
+ * The last three need d_slope.  Each row's sum of weighted gradients is taken
+ * to float32 whatever the storage type.  A pair at distance zero adds nothing
+ * to dL/dr.  Every gradient is a sum in a fixed order: deterministic, no
+ * atomics.
+ * Errors of both: EGAT_ERR_ARG, EGAT_ERR_UNSUPPORTED, EGAT_ERR_WORKSPACE,
+ * EGAT_ERR_CUDA.
+ */
+typedef struct egat_mol_shape {
+  int32_t nq;      /* query rows */
+  int32_t nk;      /* key rows (self form: = nq) */
+  int32_t n_mol;   /* molecules, >= 0 */
+  int32_t lmax;    /* highest irrep degree of the values, 0..3 */
+  int32_t C;       /* channels per degree */
+  int32_t H;       /* attention heads */
+  int32_t dk;      /* query/key width per head */
+  int32_t dtype;   /* EGAT_F32 or EGAT_BF16 */
+  float cap;       /* tanh cap of the scores, 0 = none */
+} egat_mol_shape;
+
+EGAT_API int egat_molecule_attention_workspace_bytes(const egat_mol_shape* s, size_t* bytes);
+EGAT_API int egat_molecule_attention(const egat_mol_shape* s, const void* d_q, const void* d_k,
+                                     const void* d_hp, const int32_t* d_q_ptr,
+                                     const int32_t* d_k_ptr, const float* d_pos_q,
+                                     const float* d_pos_k, const float* d_slope, void* d_ws,
+                                     size_t ws_bytes, void* d_m, float* d_lse, void* stream);
+EGAT_API int egat_molecule_attention_backward_workspace_bytes(const egat_mol_shape* s,
+                                                              size_t* bytes);
+EGAT_API int egat_molecule_attention_backward(
+    const egat_mol_shape* s, const void* d_q, const void* d_k, const void* d_hp,
+    const int32_t* d_q_ptr, const int32_t* d_k_ptr, const float* d_pos_q, const float* d_pos_k,
+    const float* d_slope, const void* d_m, const float* d_lse, const void* d_grad_m, void* d_ws,
+    size_t ws_bytes, void* d_dq, void* d_dk, void* d_dhp, float* d_dpos_q, float* d_dpos_k,
+    float* d_dslope, void* stream);
+
+/*
+ * Layer norm of rows, the normalisation in front of a projection (the
+ * degree-0 scalars feed egat_qk_projection) or of an attention block:
+ *   y_i[c] = (x_i[c] - mu_i) rstd_i weight[c] + bias[c],
+ *   mu_i = mean_c x_i[c],  rstd_i = 1 / sqrt(mean_c (x_i[c] - mu_i)^2 + eps)
+ * Rows have a stride of their own, so that the degree-0 rows of [n][D][C]
+ * features are normalised where they lie (stride D*C).
+ *  n, width   rows, 1 <= width <= 16384
+ *  dtype      EGAT_F32 or EGAT_BF16: type of x, y, the gradient and dx
+ *  ldx, ldy   row strides in elements, >= width
+ *  d_weight, d_bias  float32 [width]; NULL = ones, zeros
+ *  eps        finite, >= 0
+ *  d_y        [n] rows of width; may be d_x itself (in place)
+ *  d_stats    float32 [n][2] (mu, rstd) for the backward pass; may be NULL
+ * Mean, centred variance and all sums are float32.  n = 0 is a no-op.
+ *
+ * egat_layer_norm_backward: from x, weight, the forward's stats and the
+ * upstream gradient g, with xh = (x - mu) rstd and t = g weight,
+ *   dx = rstd (t - mean_c t - xh mean_c(t xh)),
+ *   dweight[c] = sum_i g_i[c] xh_i[c],  dbias[c] = sum_i g_i[c]
+ *  d_dx       row stride lddx; may be NULL, and may be the gradient's rows
+ *  d_dweight, d_dbias  float32 [width]; may be NULL.  n = 0 gives zeros
+ *  d_ws       at least egat_layer_norm_backward_workspace_bytes(n, width)
+ * The weight sums run in a fixed order (per-block partial sums, then one
+ * reduction): deterministic, no atomics.
+ * Pointers are aligned to their element type (16 bytes for d_ws).  Errors:
+ * EGAT_ERR_ARG, EGAT_ERR_UNSUPPORTED (width), EGAT_ERR_WORKSPACE, EGAT_ERR_CUDA.
+ */
+EGAT_API int egat_layer_norm(const void* d_x, int64_t ldx, int32_t n, int32_t width, int32_t dtype,
+                             const float* d_weight, const float* d_bias, float eps, void* d_y,
+                             int64_t ldy, float* d_stats, void* stream);
+EGAT_API int egat_layer_norm_backward_workspace_bytes(int32_t n, int32_t width, size_t* bytes);
+EGAT_API int egat_layer_norm_backward(const void* d_x, int64_t ldx, int32_t n, int32_t width,
+                                      int32_t dtype, const float* d_weight, const float* d_stats,
+                                      const void* d_grad, int64_t ldg, void* d_ws, size_t ws_bytes,
+                                      void* d_dx, int64_t lddx, float* d_dweight, float* d_dbias,
+                                      void* stream);
+
+/*
  * Row gather, the packing step of a halo exchange (a spatial domain
  * decomposition across GPUs: each rank couples its own atoms and needs the
  * h' and k rows of the neighbours it does not own; one GPU reaches about
