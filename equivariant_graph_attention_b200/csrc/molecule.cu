@@ -27,6 +27,7 @@ template <int NV, int LP>
 struct MolRows {
   static constexpr int KV = LP >= 8 ? 1 : 8 / LP;    // query vectors of a lane (dk <= 32)
   static constexpr int M = kMolWarps * (32 / LP);    // rows of a tile
+  static constexpr int MLOG = LP == 1 ? 7 : LP == 2 ? 6 : LP == 4 ? 5 : LP == 8 ? 4 : LP == 16 ? 3 : 2;
   static constexpr int DV = 4 * NV * LP;             // value columns
 };
 
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
   float* sv = sk + p.kb * p.dk;
   float* sp = sv + p.kb * R::DV;
   const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile<R::M>(p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  const MolTile t = mol_tile(R::MLOG, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
   if (t.rows <= 0) return;
   const int own = threadIdx.x / LP;
   const bool live = own < t.rows;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
   float* sp = sv + p.kb * R::DV;
   __shared__ float warp_ds[kMolWarps];
   const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile<R::M>(p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  const MolTile t = mol_tile(R::MLOG, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
   if (t.rows <= 0) {
     if (p.want_pos && threadIdx.x == 0) p.part_ds[size_t(head) * p.slots + blockIdx.x] = 0.f;
     return;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
   float* sp = sg + p.kb * R::DV;
   float* sl = sp + 4 * p.kb;   // lse2, delta
   const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile<R::M>(p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
+  const MolTile t = mol_tile(R::MLOG, p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
   if (t.rows <= 0) return;
   const int own = threadIdx.x / LP;
   const bool live = own < t.rows;
@@ -563,14 +564,42 @@ int generic_rows(const egat_mol_shape& s) {
   return m;
 }
 
-// Key splits: with fewer row tiles than four waves of 148 SMs, each
-// molecule's keys are cut so that about that many blocks run, but not below
-// 128 keys a part on average.  Depends on the shape alone.
-int key_splits(const egat_mol_shape& s, int tile_rows) {
-  if (s.n_mol == 0 || s.nk == 0) return 1;
-  const long long blocks = ((long long)s.nq / tile_rows + std::min(s.n_mol, s.nq) + 1) * s.H;
-  const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
-  return int(std::max(1LL, std::min(std::min(most, want), 64LL)));
+// How the forward pass cuts a shape: rows of a tile and key splits.  Depends on
+// the shape alone.
+struct MolCut {
+  bool tc;
+  int rwlog;    // tensor-core tiles: 16 << rwlog rows
+  int rows;     // rows of a tile
+  int groups;   // blocks side by side over heads
+  int splits;
+};
+long long tile_blocks(const egat_mol_shape& s, int rows, int groups) {
+  return ((long long)s.nq / rows + std::min(s.n_mol, s.nq)) * groups;
+}
+MolCut forward_cut(const egat_mol_shape& s) {
+  MolCut c{};
+  c.tc = mol_tc_supported(s);
+  c.groups = c.tc ? s.H / mol_tc_heads(s) : s.H;
+  c.rows = generic_rows(s);
+  if (c.tc) {
+    // 64-row tiles read the keys a quarter as often as 16-row tiles, whose four
+    // warps share the keys of one row tile instead: taken where two blocks an SM
+    // remain and the molecules are that long
+    c.rwlog = 2;
+    while (c.rwlog > 0 && (tile_blocks(s, 16 << c.rwlog, c.groups) < 2 * 148 ||
+                           (long long)s.nq < (long long)(8 << c.rwlog) * s.n_mol))
+      --c.rwlog;
+    c.rows = 16 << c.rwlog;
+  }
+  // With fewer row tiles than four waves of 148 SMs, each molecule's keys are cut
+  // so that about that many blocks run, but not below 128 keys a part on average.
+  c.splits = 1;
+  if (s.n_mol > 0 && s.nk > 0 && c.rwlog == 0) {
+    const long long blocks = std::max(1LL, tile_blocks(s, c.rows, c.groups));
+    const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
+    c.splits = int(std::max(1LL, std::min(std::min(most, want), 64LL)));
+  }
+  return c;
 }
 
 MolParams base_params(const egat_mol_shape& s, const MolArgs& a) {
@@ -598,17 +627,12 @@ size_t stage_bytes(const MolParams& p) { return size_t(p.kb) * (p.dk + p.dv + 6)
 int launched() { return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA; }
 
 template <typename T>
-int forward_t(MolParams p, cudaStream_t st) {
-  const int rc = by_rows(p.dv, [&](auto nv, auto lp) {
+int forward_t(const MolParams& p, cudaStream_t st) {
+  return by_rows(p.dv, [&](auto nv, auto lp) {
     constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value;
-    p.slots = mol_slots(p.nq, p.nmol, MolRows<NV, LP>::M);
     mol_fwd_kernel<NV, LP, T><<<dim3(p.slots, p.H, p.splits), kMolThreads, stage_bytes(p), st>>>(p);
     return launched();
   });
-  if (rc != EGAT_OK || p.splits == 1) return rc;
-  const size_t warps = size_t(p.nq) * p.H;
-  mol_join_kernel<T><<<unsigned((warps + 3) / 4), 128, 0, st>>>(p);
-  return launched();
 }
 
 template <typename T>
@@ -647,9 +671,9 @@ MolBwdWs bwd_ws(const egat_mol_shape& s, int slots) {
 }  // namespace
 
 size_t molecule_ws_bytes(const egat_mol_shape& s) {
-  const int splits = key_splits(s, generic_rows(s));
-  if (splits == 1) return 0;
-  const size_t rows = size_t(splits) * s.nq * s.H;
+  const MolCut c = forward_cut(s);
+  if (c.splits == 1) return 0;
+  const size_t rows = size_t(c.splits) * s.nq * s.H;
   return up256(rows * head_columns(s) * sizeof(float)) + up256(rows * 2 * sizeof(float));
 }
 
@@ -658,13 +682,24 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
   MolParams p = base_params(s, a);
   p.m = d_m;
   p.lse = d_lse;
-  p.splits = key_splits(s, generic_rows(s));
+  const MolCut c = forward_cut(s);
+  p.splits = c.splits;
+  p.rwlog = c.rwlog;
   if (p.splits > 1) {
     p.part_o = static_cast<float*>(d_ws);
     p.part_ml = reinterpret_cast<float*>(static_cast<char*>(d_ws) +
                                          up256(size_t(p.splits) * s.nq * s.H * p.dv * sizeof(float)));
   }
-  return s.dtype == EGAT_BF16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
+  p.slots = mol_slots(s.nq, s.n_mol, c.rows);
+  const int rc = c.tc ? mol_tc_forward(p, st)
+                      : s.dtype == EGAT_BF16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
+  if (rc != EGAT_OK || p.splits == 1) return rc;
+  const unsigned blocks = unsigned((size_t(p.nq) * p.H + 3) / 4);
+  if (s.dtype == EGAT_BF16)
+    mol_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p);
+  else
+    mol_join_kernel<float><<<blocks, 128, 0, st>>>(p);
+  return launched();
 }
 
 size_t molecule_backward_ws_bytes(const egat_mol_shape& s) {

@@ -16,8 +16,8 @@ struct MolParams {
   float* part_o;       // [splits][nq][H][dv] unnormalised sums of a key split
   float* part_ml;      // [splits][nq][H][2] its maximum (base 2) and normaliser
   float* delta;        // [nq][H] sum_j a_ij dP_ij
-  float* part_dq;      // [H][nq][3] dL/dr of the query atoms, by head
-  float* part_dk;      // [H][nk][3] dL/dr of the key atoms, by head
+  float* part_dq;      // [groups][nq][3] dL/dr of the query atoms, by group of heads
+  float* part_dk;      // [groups][nk][3] dL/dr of the key atoms
   float* part_ds;      // [H][slots] dL/dslope, by query tile
   int nq, nk, nmol, D, C, H, dk;
   int ch;              // channels of a head, C / H
@@ -26,6 +26,8 @@ struct MolParams {
   int splits;          // key splits (grid z)
   int slots;           // query tile slots
   int kb;              // keys per staged tile (generic kernels)
+  int rwlog;           // log2 of the warps side by side over rows (tensor-core kernels)
+  int groups;          // head groups with position sums of their own
   float scale;         // 1 / sqrt(dk)
   float cap, inv_cap;  // 0: none
   bool exact_delta;    // delta from a float32 sweep instead of G . m
@@ -57,16 +59,16 @@ struct MolTile {
   int row0, rows;    // own rows; rows <= 0: nothing to do
   int o0, o1;        // rows of the other side it meets
 };
-// The tile of a slot; called by whole warps (32-way bisection).
-template <int M>
-__device__ __forceinline__ MolTile mol_tile(const int32_t* ptr, const int32_t* optr, int nmol, int n,
-                                            int on, int slot) {
+// The tile of a slot (M = 2^mlog); called by whole warps (32-way bisection).
+__device__ __forceinline__ MolTile mol_tile(int mlog, const int32_t* ptr, const int32_t* optr, int nmol,
+                                            int n, int on, int slot) {
+  const int M = 1 << mlog;
   const int lane = threadIdx.x & 31;
   int lo = 0, len = nmol + 2;
   while (len > 1) {
     const int step = (len + 31) / 32;
     const int b = lo + lane * step;
-    const bool in = lane * step < len && (lane == 0 || mol_start(ptr, nmol, n, b) / M + b <= slot);
+    const bool in = lane * step < len && (lane == 0 || (mol_start(ptr, nmol, n, b) >> mlog) + b <= slot);
     const int c = 31 - __clz(int(__ballot_sync(~0u, in)));   // lane 0 is always in
     lo += c * step;
     len = min(step, len - c * step);
@@ -74,9 +76,9 @@ __device__ __forceinline__ MolTile mol_tile(const int32_t* ptr, const int32_t* o
   MolTile t;
   const int s = mol_start(ptr, nmol, n, lo), e = mol_start(ptr, nmol, n, lo + 1);
   // pointers that descend give a segment more slots than it has rows: those stay empty
-  const int off = slot - (s / M + lo);
-  const bool some = e > s && off <= (e - s) / M;
-  t.row0 = some ? s + off * M : 0;
+  const int off = slot - ((s >> mlog) + lo);
+  const bool some = e > s && off <= ((e - s) >> mlog);
+  t.row0 = some ? s + (off << mlog) : 0;
   t.rows = some ? min(M, e - t.row0) : 0;
   const bool mol = lo > 0 && lo <= nmol;
   t.o0 = mol ? mol_start(optr, nmol, on, lo) : 0;
@@ -104,5 +106,13 @@ __device__ __forceinline__ float mol_sqrt(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// Tensor-core kernels (bf16 storage): value tiles of 8 columns a head they
+// take, and their launches.  rows = rows of a tile, 16 << p.rwlog.
+bool mol_tc_supported(const egat_mol_shape& s);
+int mol_tc_heads(const egat_mol_shape& s);   // heads a warp takes together
+int mol_tc_forward(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_q(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_k(const MolParams& p, cudaStream_t st);
 
 }  // namespace egat
