@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
   }
 }
 
-// dL/dr summed over heads (and, in the self form, over both roles of an
+// dL/dr summed over groups of heads (and, in the self form, over both roles of an
 // atom); the last H blocks sum dL/dslope over query tiles, in a fixed order.
 __global__ void mol_reduce_kernel(MolParams p, int pos_blocks) {
   if (int(blockIdx.x) < pos_blocks) {
@@ -493,7 +493,7 @@ __global__ void mol_reduce_kernel(MolParams p, int pos_blocks) {
     const long long j = p.a.self ? i : i - nq3;
     if (i < nq3 && p.g.dposq) {
       float s = 0.f;
-      for (int h = 0; h < p.H; ++h) {
+      for (int h = 0; h < p.groups; ++h) {
         s += p.part_dq[h * nq3 + i];
         if (p.a.self) s += p.part_dk[h * nk3 + i];
       }
@@ -501,7 +501,7 @@ __global__ void mol_reduce_kernel(MolParams p, int pos_blocks) {
     }
     if (!p.a.self && j >= 0 && j < nk3 && p.g.dposk) {
       float s = 0.f;
-      for (int h = 0; h < p.H; ++h) s += p.part_dk[h * nk3 + j];
+      for (int h = 0; h < p.groups; ++h) s += p.part_dk[h * nk3 + j];
       p.g.dposk[j] = s;
     }
     return;
@@ -573,29 +573,29 @@ struct MolCut {
   int groups;   // blocks side by side over heads
   int splits;
 };
-long long tile_blocks(const egat_mol_shape& s, int rows, int groups) {
-  return ((long long)s.nq / rows + std::min(s.n_mol, s.nq)) * groups;
+long long tile_blocks(int n, int n_mol, int rows, int groups) {
+  return ((long long)n / rows + std::min(n_mol, n)) * groups;
+}
+// 64-row tiles read the other side's rows a quarter as often as 16-row tiles,
+// whose four warps share those rows of one row tile instead: taken where two
+// blocks an SM remain and the molecules are that long.
+int tc_rwlog(int n, int n_mol, int groups) {
+  int l = 2;
+  while (l > 0 && (tile_blocks(n, n_mol, 16 << l, groups) < 2 * 148 || (long long)n < (long long)(8 << l) * n_mol))
+    --l;
+  return l;
 }
 MolCut forward_cut(const egat_mol_shape& s) {
   MolCut c{};
   c.tc = mol_tc_supported(s);
   c.groups = c.tc ? s.H / mol_tc_heads(s) : s.H;
-  c.rows = generic_rows(s);
-  if (c.tc) {
-    // 64-row tiles read the keys a quarter as often as 16-row tiles, whose four
-    // warps share the keys of one row tile instead: taken where two blocks an SM
-    // remain and the molecules are that long
-    c.rwlog = 2;
-    while (c.rwlog > 0 && (tile_blocks(s, 16 << c.rwlog, c.groups) < 2 * 148 ||
-                           (long long)s.nq < (long long)(8 << c.rwlog) * s.n_mol))
-      --c.rwlog;
-    c.rows = 16 << c.rwlog;
-  }
+  c.rwlog = c.tc ? tc_rwlog(s.nq, s.n_mol, c.groups) : 0;
+  c.rows = c.tc ? 16 << c.rwlog : generic_rows(s);
   // With fewer row tiles than four waves of 148 SMs, each molecule's keys are cut
   // so that about that many blocks run, but not below 128 keys a part on average.
   c.splits = 1;
   if (s.n_mol > 0 && s.nk > 0 && c.rwlog == 0) {
-    const long long blocks = std::max(1LL, tile_blocks(s, c.rows, c.groups));
+    const long long blocks = std::max(1LL, tile_blocks(s.nq, s.n_mol, c.rows, c.groups));
     const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
     c.splits = int(std::max(1LL, std::min(std::min(most, want), 64LL)));
   }
@@ -636,10 +636,9 @@ int forward_t(const MolParams& p, cudaStream_t st) {
 }
 
 template <typename T>
-int backward_t(MolParams p, cudaStream_t st) {
+int backward_t(const MolParams& p, cudaStream_t st) {
   return by_rows(p.dv, [&](auto nv, auto lp) {
     constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value, M = MolRows<NV, LP>::M;
-    p.slots = mol_slots(p.nq, p.nmol, M);
     if (p.nq > 0) {
       mol_bwd_q_kernel<NV, LP, T><<<dim3(p.slots, p.H), kMolThreads, stage_bytes(p), st>>>(p);
       if (launched() != EGAT_OK) return int(EGAT_ERR_CUDA);
@@ -656,15 +655,19 @@ int backward_t(MolParams p, cudaStream_t st) {
 // Workspace of the backward pass: delta, then the partial sums of the
 // position and slope gradients.
 struct MolBwdWs {
+  MolCut cut;
+  int slots;
   size_t delta, dq, dk, ds, total;
 };
-MolBwdWs bwd_ws(const egat_mol_shape& s, int slots) {
+MolBwdWs bwd_ws(const egat_mol_shape& s) {
   MolBwdWs w;
+  w.cut = forward_cut(s);
+  w.slots = mol_slots(s.nq, s.n_mol, w.cut.rows);
   w.delta = 0;
   w.dq = up256(sizeof(float) * size_t(s.nq) * s.H);
-  w.dk = w.dq + up256(sizeof(float) * 3 * size_t(s.nq) * s.H);
-  w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * s.H);
-  w.total = w.ds + up256(sizeof(float) * size_t(slots) * s.H);
+  w.dk = w.dq + up256(sizeof(float) * 3 * size_t(s.nq) * w.cut.groups);
+  w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * w.cut.groups);
+  w.total = w.ds + up256(sizeof(float) * size_t(w.slots) * s.H);
   return w;
 }
 
@@ -703,15 +706,14 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
 }
 
 size_t molecule_backward_ws_bytes(const egat_mol_shape& s) {
-  return bwd_ws(s, mol_slots(s.nq, s.n_mol, generic_rows(s))).total;
+  return bwd_ws(s).total;
 }
 
 int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const MolGrads& g,
                              void* d_ws, cudaStream_t st) {
   MolParams p = base_params(s, a);
   p.g = g;
-  const int slots = mol_slots(s.nq, s.n_mol, generic_rows(s));
-  const MolBwdWs w = bwd_ws(s, slots);
+  const MolBwdWs w = bwd_ws(s);
   char* base = static_cast<char*>(d_ws);
   p.delta = reinterpret_cast<float*>(base + w.delta);
   p.part_dq = reinterpret_cast<float*>(base + w.dq);
@@ -721,8 +723,17 @@ int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const Mo
   // float32 m gives delta to float32; bf16 m would leave it bf16's error, which
   // showed as 1.6 times the rounding error of dq (4,096 atoms, 16 heads)
   p.exact_delta = s.dtype == EGAT_BF16;
-  p.slots = slots;
-  const int rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, st) : backward_t<float>(p, st);
+  p.slots = w.slots;
+  p.groups = w.cut.groups;
+  p.rwlog = w.cut.rwlog;
+  int rc = EGAT_OK;
+  if (w.cut.tc) {
+    if (s.nq > 0) rc = mol_tc_backward_q(p, st);
+    p.rwlog = tc_rwlog(s.nk, s.n_mol, p.groups);
+    if (rc == EGAT_OK && s.nk > 0) rc = mol_tc_backward_k(p, st);
+  } else {
+    rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, st) : backward_t<float>(p, st);
+  }
   if (rc != EGAT_OK || !p.want_pos) return rc;
   if (s.nq == 0) {   // no query tile ran
     if (g.dslope && cudaMemsetAsync(g.dslope, 0, sizeof(float) * s.H, st) != cudaSuccess)

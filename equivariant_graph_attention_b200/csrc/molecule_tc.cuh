@@ -243,6 +243,19 @@ __device__ __forceinline__ void tc_cap(f32x2& a, f32x2& b, f32x2& fa, f32x2& fb)
   }
 }
 
+// Two distances from their squares and, with RECIP, their reciprocals (any finite
+// number at distance zero, where the direction is zero).
+template <bool RECIP>
+__device__ __forceinline__ void tc_dist(float a, float b, f32x2& d, f32x2& ri) {
+  if (!RECIP) {
+    d = f2_pack(mol_sqrt(a), mol_sqrt(b));
+    return;
+  }
+  const float ra = rsqrtf(fminf(fmaxf(a, 1e-37f), 3.4e38f)), rb = rsqrtf(fminf(fmaxf(b, 1e-37f), 3.4e38f));
+  ri = f2_pack(ra, rb);
+  d = f2_mul(f2_pack(a, b), ri);   // NaN and inf of the squares stay
+}
+
 // Calls f with the value tiles, the query chunks and the heads of a warp.
 template <typename F>
 int tc_dispatch(int nt, int dk, F&& f) {
