@@ -652,19 +652,20 @@ int backward_t(const MolParams& p, cudaStream_t st) {
   });
 }
 
-// Workspace of the backward pass: delta, then the partial sums of the
+// Workspace of the backward pass: delta (and lse in base 2), then the partial sums of the
 // position and slope gradients.
 struct MolBwdWs {
   MolCut cut;
   int slots;
-  size_t delta, dq, dk, ds, total;
+  size_t delta, nlse2, dq, dk, ds, total;
 };
 MolBwdWs bwd_ws(const egat_mol_shape& s) {
   MolBwdWs w;
   w.cut = forward_cut(s);
   w.slots = mol_slots(s.nq, s.n_mol, w.cut.rows);
   w.delta = 0;
-  w.dq = up256(sizeof(float) * size_t(s.nq) * s.H);
+  w.nlse2 = up256(sizeof(float) * size_t(s.nq) * s.H);
+  w.dq = w.nlse2 + (w.cut.tc ? w.nlse2 : 0);
   w.dk = w.dq + up256(sizeof(float) * 3 * size_t(s.nq) * w.cut.groups);
   w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * w.cut.groups);
   w.total = w.ds + up256(sizeof(float) * size_t(w.slots) * s.H);
@@ -716,6 +717,7 @@ int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const Mo
   const MolBwdWs w = bwd_ws(s);
   char* base = static_cast<char*>(d_ws);
   p.delta = reinterpret_cast<float*>(base + w.delta);
+  p.nlse2 = reinterpret_cast<float*>(base + w.nlse2);
   p.part_dq = reinterpret_cast<float*>(base + w.dq);
   p.part_dk = reinterpret_cast<float*>(base + w.dk);
   p.part_ds = reinterpret_cast<float*>(base + w.ds);

@@ -15,7 +15,8 @@ struct MolParams {
   float* lse;
   float* part_o;       // [splits][nq][H][dv] unnormalised sums of a key split
   float* part_ml;      // [splits][nq][H][2] its maximum (base 2) and normaliser
-  float* delta;        // [nq][H] sum_j a_ij dP_ij
+  float* delta;        // [nq][H] sum_j a_ij dP_ij (minus that on the tensor-core path)
+  float* nlse2;        // [nq][H] minus lse in base 2, -inf for rows without weights (tensor-core path)
   float* part_dq;      // [groups][nq][3] dL/dr of the query atoms, by group of heads
   float* part_dk;      // [groups][nk][3] dL/dr of the key atoms
   float* part_ds;      // [H][slots] dL/dslope, by query tile
@@ -101,9 +102,10 @@ __device__ __forceinline__ float mol_tanh(float x, float& slope) {
   r = fmaf(y, r, -1.f / 3.f);
   return fabsf(x) < 0.3f ? fmaf(x * y, r, x) : copysignf(fmaf(-2.f, u, 1.f), x);
 }
+// squares below 2^-126 count as zero
 __device__ __forceinline__ float mol_sqrt(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 

@@ -9,7 +9,7 @@ namespace {
 // and meets the molecule's query rows.  The products are transposed (S^T = K Q^T,
 // dP^T = H' G^T), so that the weights and dS land as the A operands of
 // dh' = a^T G and dk = dS^T Q.  A query row past the molecule has lse2 = +inf: no weight.
-template <int NT, int KC, int HP, bool POS>
+template <int NT, int KC, int HP, bool CAP, bool BIAS, bool POS>
 __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP>;
   // the key rows' values as A fragments: in registers, or read again for every
@@ -28,20 +28,27 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
   const __nv_bfloat16* gm = static_cast<const __nv_bfloat16*>(p.g.g);
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.hp);
   const uint32_t sbase = tc_smem(tsm);
+  TcLoader<NT, KC, HP> ld;
   auto load = [&](int r0, int b) {
     const uint32_t st = sbase + b * L::STAGE;
-    tc_load_stage<NT, KC, HP>(p, q, gm, p.a.posq, head0, r0, t.o1, st);
-    float* sl = reinterpret_cast<float*>(tsm + b * L::STAGE + L::ROW);
+    ld.load(st, t.o1 - r0);
+    // minus lse2 and delta of the query rows; no weight past the molecule
     for (int i = threadIdx.x; i < kTcStage * HP; i += kTcThreads) {
-      const int r = i / HP, h = i % HP;
-      const bool ok = r0 + r < t.o1;
+      const int r = i / HP, h = i % HP, o = L::ROW + (h * 2 * kTcStage + r) * 4;
       const size_t at = size_t(r0 + r) * p.H + head0 + h;
-      const float x = ok ? p.g.lse[at] * kLog2e : INFINITY;
-      sl[h * 2 * kTcStage + r] = x == -INFINITY ? -INFINITY : -x;   // minus lse2
-      sl[h * 2 * kTcStage + kTcStage + r] = ok ? -p.delta[at] : 0.f;
+      if (r0 + r < t.o1) {
+        tc_cp4(st + o, p.nlse2 + at, true);
+        tc_cp4(st + o + kTcStage * 4, p.delta + at, true);
+      } else {
+        *reinterpret_cast<float*>(tsm + b * L::STAGE + o) = -INFINITY;
+        *reinterpret_cast<float*>(tsm + b * L::STAGE + o + kTcStage * 4) = 0.f;
+      }
     }
   };
-  if (t.o0 < t.o1) load(t.o0, 0);
+  if (t.o0 < t.o1) {
+    ld.init(p, q, gm, p.a.posq, head0, t.o0);
+    load(t.o0, 0);
+  }
   tc_commit();
 
   uint32_t kf[HP][KC][2], vf[HP][VREG ? NT : 1][2];
@@ -50,9 +57,9 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
   for (int h = 0; h < HP; ++h) {
     tc_frag_qk<KC>(p, static_cast<const __nv_bfloat16*>(p.a.k), rowA, rowB, lA, lB, head0 + h, kf[h]);
     if constexpr (VREG) tc_frag_val<NT>(p, v, rowA, rowB, lA, lB, head0 + h, vf[h]);
-    if (p.a.slope) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
+    if constexpr (BIAS) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
   }
-  if (p.a.slope)
+  if constexpr (BIAS)
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (r ? lB : lA) {
@@ -61,10 +68,10 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
         py[r] = f2_set(-x[1]);
         pz[r] = f2_set(-x[2]);
       }
-  const bool capped = p.cap > 0.f;
-  const f32x2 c_in = f2_set(capped ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
+  const f32x2 c_in = f2_set(CAP ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
 
-  float dk[HP][KC][4] = {}, dv[HP][NT][4] = {}, gs[2][3] = {};
+  float dk[HP][KC][4] = {}, dv[HP][NT][4] = {};
+  f32x2 gs[2][3] = {};
   int buf = 0;
   for (int q0 = t.o0; q0 < t.o1; q0 += kTcStage, buf ^= 1) {
     if (q0 + kTcStage < t.o1) load(q0 + kTcStage, buf ^ 1);
@@ -79,20 +86,7 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
 #pragma unroll 1
       for (int j = kw * 16; j < n; j += kws * 16) {
         f32x2 d[2][2] = {}, ri[2][2] = {};
-        if (p.a.slope) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-            const f32x2 x = at[0], y = at[kTcStage / 2], z = at[kTcStage];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const f32x2 dx = f2_add(x, px[r]), dy = f2_add(y, py[r]), dz = f2_add(z, pz[r]);
-              float a, b;
-              f2_unpack(f2_fma(dx, dx, f2_fma(dy, dy, f2_mul(dz, dz))), a, b);
-              tc_dist<POS>(a, b, d[c][r], ri[c][r]);
-            }
-          }
-        }
+        if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
         f32x2 u[2][2] = {};   // POS: sum over the heads of slope dS
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
@@ -111,35 +105,37 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
                 a[e][0] = lA ? __ldg(reinterpret_cast<const uint32_t*>(v + rowA * (p.D * p.C) + o)) : 0u;
                 a[e][1] = lB ? __ldg(reinterpret_cast<const uint32_t*>(v + rowB * (p.D * p.C) + o)) : 0u;
               }
-              tc_dot<2>(dp, a, gb + c * HP * 16 + tc_lane_n(L::RV, HP * 16), 0, HP * 16);
+              tc_dot<2, true>(dp, a, gb + c * HP * 16 + tc_lane_n(L::RV, HP * 16), 0, HP * 16);
             }
+          }
+          f32x2 x[4], fx[CAP ? 4 : 1];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            x[2 * c] = f2_pack(s[c][0], s[c][1]);
+            x[2 * c + 1] = f2_pack(s[c][2], s[c][3]);
+          }
+          if constexpr (CAP) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
+            tc_cap<4, true>(x, fx);
           }
           uint32_t fd[2][2], fa[2][2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int i = 0; i < 4; ++i) {
+            const int c = i >> 1, r = i & 1;
             const f32x2* row = reinterpret_cast<const f32x2*>(sl + h * 2 * kTcStage + j + 8 * c + t2);
-            const f32x2 lse = row[0], del = row[kTcStage / 2];
-            f32x2 x[2] = {f2_pack(s[c][0], s[c][1]), f2_pack(s[c][2], s[c][3])}, fx[2];
-            if (capped) {
-              x[0] = f2_mul(x[0], c_in);
-              x[1] = f2_mul(x[1], c_in);
-              tc_cap<true>(x[0], x[1], fx[0], fx[1]);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              x[r] = f2_fma(x[r], capped ? c_cap : c_in, lse);
-              if (p.a.slope) x[r] = f2_fma(d[c][r], slope[h], x[r]);
-              float a, b;
-              f2_unpack(x[r], a, b);
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-              fa[c][r] = tc_pack(a, b);
-              f32x2 ds = f2_mul(f2_pack(a, b), f2_add(f2_pack(dp[c][2 * r], dp[c][2 * r + 1]), del));
-              if (POS) u[c][r] = f2_fma(ds, slope[h], u[c][r]);
-              if (capped) ds = f2_mul(ds, fx[r]);
-              f2_unpack(ds, a, b);
-              fd[c][r] = tc_pack(a, b);
-            }
+            x[i] = f2_fma(x[i], CAP ? c_cap : c_in, row[0]);
+            if constexpr (BIAS) x[i] = f2_fma(d[c][r], slope[h], x[i]);
+            float a, b;
+            f2_unpack(x[i], a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            fa[c][r] = tc_pack(a, b);
+            f32x2 ds = f2_mul(f2_pack(a, b), f2_add(f2_pack(dp[c][2 * r], dp[c][2 * r + 1]), row[kTcStage / 2]));
+            if (POS) u[c][r] = f2_fma(ds, slope[h], u[c][r]);
+            if constexpr (CAP) ds = f2_mul(ds, fx[i]);
+            f2_unpack(ds, a, b);
+            fd[c][r] = tc_pack(a, b);
           }
           tc_apply<NT>(dv[h], fa, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16);
           tc_apply<KC>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16);
@@ -153,11 +149,7 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
               const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
               const f32x2 f = f2_mul(u[c][r], ri[c][r]);
 #pragma unroll
-              for (int e = 0; e < 3; ++e) {
-                float lo, hi;
-                f2_unpack(f2_mul(f, dir[e]), lo, hi);
-                gs[r][e] += lo + hi;
-              }
+              for (int e = 0; e < 3; ++e) gs[r][e] = f2_fma(f, dir[e], gs[r][e]);
             }
           }
         }
@@ -188,7 +180,9 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
     if constexpr (POS)
 #pragma unroll
       for (int e = 0; e < 3; ++e) {
-        const float x = quad_sum(gs[r][e]);
+        float g0, g1;
+        f2_unpack(gs[r][e], g0, g1);
+        const float x = quad_sum(g0 + g1);
         if (t2 == 0) o[row * ROW + QN + e] = x;
       }
   }
@@ -236,8 +230,15 @@ int mol_tc_backward_k(const MolParams& p, cudaStream_t st) {
     const size_t join = 4 * 16 * (L::OUTROW + HP * KC * 8 + 4) * 4;
     const size_t shm = std::max(size_t(2 * L::STAGE), join);
     const dim3 grid(mol_slots(p.nk, p.nmol, 16 << p.rwlog), p.H / HP);
-    return p.want_pos ? tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, true>, grid, shm, p, st)
-                      : tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, false>, grid, shm, p, st);
+    // positions come with a bias
+    if (p.want_pos)
+      return mol_flags(p.cap > 0.f, true, [&](auto cap, auto) {
+        return tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, decltype(cap)::value, true, true>, grid, shm, p, st);
+      });
+    return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
+      return tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value, false>, grid, shm, p,
+                       st);
+    });
   });
 }
 

@@ -12,7 +12,7 @@ namespace {
 //   dq = sum dS' f' k + (delta' - delta) sum a f' k,
 // so the second sum, of weights alone, takes the rounding of m out at the end;
 // the correction is small, so nothing cancels.
-template <int NT, int KC, int HP, bool POS>
+template <int NT, int KC, int HP, bool CAP, bool BIAS, bool POS>
 __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP>;
   extern __shared__ __align__(128) unsigned char tsm[];
@@ -30,7 +30,11 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.a.k);
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.hp);
   const uint32_t sbase = tc_smem(tsm);
-  if (t.o0 < t.o1) tc_load_stage<NT, KC, HP>(p, k, v, p.a.posk, head0, t.o0, t.o1, sbase);
+  TcLoader<NT, KC, HP> ld;
+  if (t.o0 < t.o1) {
+    ld.init(p, k, v, p.a.posk, head0, t.o0);
+    ld.load(sbase, t.o1 - t.o0);
+  }
   tc_commit();
 
   uint32_t qf[HP][KC][2], gf[HP][NT][2];
@@ -62,9 +66,9 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
       const float x = ok ? p.g.lse[(r ? rowB : rowA) * p.H + head0 + h] * kLog2e : INFINITY;
       lse2[h][r] = x == -INFINITY ? INFINITY : x;
     }
-    if (p.a.slope) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
+    if constexpr (BIAS) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
   }
-  if (p.a.slope)
+  if constexpr (BIAS)
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (r ? lB : lA) {
@@ -73,18 +77,26 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
         py[r] = f2_set(-x[1]);
         pz[r] = f2_set(-x[2]);
       }
-  const bool capped = p.cap > 0.f;
-  const f32x2 c_in = f2_set(capped ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
+  const f32x2 c_in = f2_set(CAP ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
+  f32x2 nlse[HP][2], ndel[HP][2];   // minus lse2 and delta'
+#pragma unroll
+  for (int h = 0; h < HP; ++h)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      nlse[h][r] = f2_set(-lse2[h][r]);
+      ndel[h][r] = f2_set(-dlt[h][r]);
+    }
 
   float dq[HP][KC][4] = {}, bk[HP][KC][4] = {};
   f32x2 del[HP][2] = {};
   // POS: sums over j of (slope dS', slope a) (r_j - r_i) / d and of (dS', a) d
-  float gs[2][3] = {}, ga[HP][2][3] = {}, sd[HP][2] = {}, sa[HP][2] = {};
+  f32x2 gs[2][3] = {}, ga[HP][2][3] = {};
+  float sd[HP][2] = {}, sa[HP][2] = {};
 
   int buf = 0;
   for (int k0 = t.o0; k0 < t.o1; k0 += kTcStage, buf ^= 1) {
     if (k0 + kTcStage < t.o1)
-      tc_load_stage<NT, KC, HP>(p, k, v, p.a.posk, head0, k0 + kTcStage, t.o1, sbase + (buf ^ 1) * L::STAGE);
+      ld.load(sbase + (buf ^ 1) * L::STAGE, t.o1 - k0 - kTcStage);
     tc_commit();
     tc_wait<1>();
     __syncthreads();
@@ -95,76 +107,67 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
 #pragma unroll 1
       for (int j = kw * 16; j < n; j += kws * 16) {
         f32x2 d[2][2] = {}, ri[2][2] = {};   // distances (and their reciprocals): [8-key tile][row]
-        if (p.a.slope) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-            const f32x2 x = at[0], y = at[kTcStage / 2], z = at[kTcStage];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const f32x2 dx = f2_add(x, px[r]), dy = f2_add(y, py[r]), dz = f2_add(z, pz[r]);
-              float a, b;
-              f2_unpack(f2_fma(dx, dx, f2_fma(dy, dy, f2_mul(dz, dz))), a, b);
-              tc_dist<POS>(a, b, d[c][r], ri[c][r]);
-            }
-          }
-        }
+        if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
           float s[2][4] = {}, dp[2][4] = {};
           tc_dot<KC>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
           const uint32_t vb = st + L::VAL + j * L::RV + h * 16;
           tc_dot<NT>(dp, gf[h], vb + tc_lane_n(L::RV, HP * 16), vb + tc_lane_n2(L::RV), HP * 16);
-          uint32_t fd[2][2], fa[2][2];
+          f32x2 x[4], fx[CAP ? 4 : 1];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            f32x2 x[2] = {f2_pack(s[c][0], s[c][1]), f2_pack(s[c][2], s[c][3])}, fx[2];
-            if (capped) {
-              x[0] = f2_mul(x[0], c_in);
-              x[1] = f2_mul(x[1], c_in);
-              tc_cap<true>(x[0], x[1], fx[0], fx[1]);
-            }
+            x[2 * c] = f2_pack(s[c][0], s[c][1]);
+            x[2 * c + 1] = f2_pack(s[c][2], s[c][3]);
+          }
+          if constexpr (CAP) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              x[r] = f2_fma(x[r], capped ? c_cap : c_in, f2_set(-lse2[h][r]));
-              if (p.a.slope) x[r] = f2_fma(d[c][r], slope[h], x[r]);
-              float a, b;
-              f2_unpack(x[r], a, b);
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-              if (j + 16 > n) {   // keys past the molecule
-                if (j + 8 * c + t2 >= n) a = 0.f;
-                if (j + 8 * c + t2 + 1 >= n) b = 0.f;
-              }
-              const f32x2 w = f2_pack(a, b), dP = f2_pack(dp[c][2 * r], dp[c][2 * r + 1]);
-              del[h][r] = f2_fma(w, dP, del[h][r]);
-              const f32x2 ds = f2_mul(w, f2_add(dP, f2_set(-dlt[h][r])));
-              if (POS) {
-                const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-                const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
-                const f32x2 wr = f2_mul(w, ri[c][r]), dr = f2_mul(f2_mul(ds, slope[h]), ri[c][r]);
-                float lo, hi;
+            for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
+            tc_cap<4, true>(x, fx);
+          }
+          uint32_t fd[2][2], fa[2][2];
 #pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                  f2_unpack(f2_mul(dr, dir[e]), lo, hi);
-                  gs[r][e] += lo + hi;
-                  f2_unpack(f2_mul(wr, dir[e]), lo, hi);
-                  ga[h][r][e] += lo + hi;
-                }
-                // d may be inf where the weight is zero
-                float d0, d1;
-                f2_unpack(d[c][r], d0, d1);
-                sa[h][r] += (a != 0.f ? a * d0 : 0.f) + (b != 0.f ? b * d1 : 0.f);
-                f2_unpack(ds, lo, hi);
-                sd[h][r] += (lo != 0.f ? lo * d0 : 0.f) + (hi != 0.f ? hi * d1 : 0.f);
-              }
-              const f32x2 yd = capped ? f2_mul(ds, fx[r]) : ds, ya = capped ? f2_mul(w, fx[r]) : w;
-              float lo, hi;
-              f2_unpack(yd, lo, hi);
-              fd[c][r] = tc_pack(lo, hi);
-              f2_unpack(ya, lo, hi);
-              fa[c][r] = tc_pack(lo, hi);
+          for (int i = 0; i < 4; ++i) {
+            const int c = i >> 1, r = i & 1;
+            x[i] = f2_fma(x[i], CAP ? c_cap : c_in, nlse[h][r]);
+            if constexpr (BIAS) x[i] = f2_fma(d[c][r], slope[h], x[i]);
+            float a, b;
+            f2_unpack(x[i], a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            if (j + 16 > n) {   // keys past the molecule
+              if (j + 8 * c + t2 >= n) a = 0.f;
+              if (j + 8 * c + t2 + 1 >= n) b = 0.f;
             }
+            f32x2 w = f2_pack(a, b);
+            const f32x2 dP = f2_pack(dp[c][2 * r], dp[c][2 * r + 1]);
+            del[h][r] = f2_fma(w, dP, del[h][r]);
+            f32x2 ds = f2_mul(w, f2_add(dP, ndel[h][r]));
+            float lo, hi;
+            if (POS) {
+              const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
+              const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
+              const f32x2 wr = f2_mul(w, ri[c][r]), dr = f2_mul(f2_mul(ds, slope[h]), ri[c][r]);
+#pragma unroll
+              for (int e = 0; e < 3; ++e) {
+                gs[r][e] = f2_fma(dr, dir[e], gs[r][e]);
+                ga[h][r][e] = f2_fma(wr, dir[e], ga[h][r][e]);
+              }
+              // d may be inf where the weight is zero
+              float d0, d1;
+              f2_unpack(d[c][r], d0, d1);
+              sa[h][r] += (a != 0.f ? a * d0 : 0.f) + (b != 0.f ? b * d1 : 0.f);
+              f2_unpack(ds, lo, hi);
+              sd[h][r] += (lo != 0.f ? lo * d0 : 0.f) + (hi != 0.f ? hi * d1 : 0.f);
+            }
+            if constexpr (CAP) {
+              ds = f2_mul(ds, fx[i]);
+              w = f2_mul(w, fx[i]);
+              f2_unpack(w, a, b);
+            }
+            f2_unpack(ds, lo, hi);
+            fd[c][r] = tc_pack(lo, hi);
+            fa[c][r] = tc_pack(a, b);
           }
           const uint32_t kb = st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16);
 #pragma unroll
@@ -209,7 +212,9 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
         if (t2 == 0) x[2] = v0, x[3] = v1;
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
-          const float v2 = quad_sum(ga[h][r][e]);
+          float g0, g1;
+          f2_unpack(ga[h][r][e], g0, g1);
+          const float v2 = quad_sum(g0 + g1);
           if (t2 == 0) x[4 + e] = v2;
         }
       }
@@ -217,7 +222,9 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
     if constexpr (POS)
 #pragma unroll
       for (int e = 0; e < 3; ++e) {
-        const float v3 = quad_sum(gs[r][e]);
+        float g0, g1;
+        f2_unpack(gs[r][e], g0, g1);
+        const float v3 = quad_sum(g0 + g1);
         if (t2 == 0) at[2 * QN + HP * PER + e] = v3;
       }
   }
@@ -244,7 +251,10 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
   }
   for (int i = threadIdx.x; i < t.rows * HP; i += kTcThreads) {
     const int row = i / HP, h = i % HP;
-    p.delta[(size_t(t.row0) + row) * p.H + head0 + h] = sum_at(row, 2 * QN + h * PER);
+    const size_t at = (size_t(t.row0) + row) * p.H + head0 + h;
+    const float x = p.g.lse[at] * kLog2e;
+    p.delta[at] = -sum_at(row, 2 * QN + h * PER);
+    p.nlse2[at] = x == -INFINITY ? -INFINITY : -x;   // a row without weights stays without
   }
   if constexpr (POS) {
     // positions: slope here is -slope log2 e, and the directions point from i to j:
@@ -281,8 +291,15 @@ int mol_tc_backward_q(const MolParams& p, cudaStream_t st) {
     const size_t join = 4 * 16 * (2 * HP * KC * 8 + HP * 7 + 4) * 4;
     const size_t shm = std::max(size_t(2 * L::STAGE), join);
     const dim3 grid(p.slots, p.H / HP);
-    return p.want_pos ? tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, true>, grid, shm, p, st)
-                      : tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, false>, grid, shm, p, st);
+    // positions come with a bias
+    if (p.want_pos)
+      return mol_flags(p.cap > 0.f, true, [&](auto cap, auto) {
+        return tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, decltype(cap)::value, true, true>, grid, shm, p, st);
+      });
+    return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
+      return tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value, false>, grid, shm, p,
+                       st);
+    });
   });
 }
 

@@ -7,11 +7,12 @@ namespace {
 
 // Per 16 x 16 pairs and head: S = Q K^T (one k-step of 16, two at dk 32), base-2
 // scores in packed float32 pairs, the online softmax, and m += P H' with P
-// rounded once to bf16 (the normaliser adds the unrounded weights).  The running
-// maximum is a reference: it moves only when a score passes it by 2^8, so most
-// steps need no exchange between lanes and no rescaling.
-template <int NT, int KC, int HP>
-__global__ void __launch_bounds__(kTcThreads) mol_fwd_tc_kernel(MolParams p) {
+// rounded once to bf16 (the normaliser adds the unrounded weights).  A row's
+// reference moves only when a score passes it by 2^8, so most steps need no
+// exchange between lanes and no rescaling; the rare step that moves it works its
+// scores out again, which keeps them out of the registers in between.
+template <int NT, int KC, int HP, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP>;
   extern __shared__ __align__(128) unsigned char tsm[];
   const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -31,14 +32,18 @@ __global__ void __launch_bounds__(kTcThreads) mol_fwd_tc_kernel(MolParams p) {
   const int k_begin = t.o0 + int(blockIdx.z) * per * kTcStage;
   const int k_end = min(t.o1, k_begin + per * kTcStage);
   const uint32_t sbase = tc_smem(tsm);
-  if (k_begin < k_end) tc_load_stage<NT, KC, HP>(p, k, v, p.a.posk, head0, k_begin, k_end, sbase);
+  TcLoader<NT, KC, HP> ld;
+  if (k_begin < k_end) {
+    ld.init(p, k, v, p.a.posk, head0, k_begin);
+    ld.load(sbase, k_end - k_begin);
+  }
   tc_commit();
 
   uint32_t qf[HP][KC][2];
 #pragma unroll
   for (int h = 0; h < HP; ++h) tc_frag_qk<KC>(p, q, rowA, rowB, lA, lB, head0 + h, qf[h]);
   f32x2 px[2] = {}, py[2] = {}, pz[2] = {}, slope[HP] = {};   // minus the rows' positions
-  if (p.a.slope) {
+  if constexpr (BIAS) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (r ? lB : lA) {
@@ -50,18 +55,19 @@ __global__ void __launch_bounds__(kTcThreads) mol_fwd_tc_kernel(MolParams p) {
 #pragma unroll
     for (int h = 0; h < HP; ++h) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
   }
-  const bool capped = p.cap > 0.f;
-  const f32x2 c_in = f2_set(capped ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
+  const f32x2 c_in = f2_set(CAP ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
 
   float acc[HP][NT][4] = {};
-  float mx[HP][2], sum[HP][2];
+  // minus the rows' references (NaN: none yet, which no score passes), and the
+  // normaliser by lane
+  f32x2 ref[HP][2], sum[HP][2] = {};
 #pragma unroll
-  for (int h = 0; h < HP; ++h) mx[h][0] = mx[h][1] = -INFINITY, sum[h][0] = sum[h][1] = 0.f;
+  for (int h = 0; h < HP; ++h) ref[h][0] = ref[h][1] = f2_set(__int_as_float(0x7fffffff));
 
   int buf = 0;
   for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= 1) {
     if (k0 + kTcStage < k_end)
-      tc_load_stage<NT, KC, HP>(p, k, v, p.a.posk, head0, k0 + kTcStage, k_end, sbase + (buf ^ 1) * L::STAGE);
+      ld.load(sbase + (buf ^ 1) * L::STAGE, k_end - k0 - kTcStage);
     tc_commit();
     tc_wait<1>();
     __syncthreads();
@@ -71,93 +77,97 @@ __global__ void __launch_bounds__(kTcThreads) mol_fwd_tc_kernel(MolParams p) {
     if (warp_live)
 #pragma unroll 1
       for (int j = kw * 16; j < n; j += kws * 16) {
-        f32x2 d[2][2] = {};   // distances: [8-key tile][row]
-        if (p.a.slope) {
+        f32x2 d[2][2] = {}, unused[2][2];
+        if constexpr (BIAS) tc_dists<false>(sp + j + t2, px, py, pz, d, unused);
+        // base-2 scores of head h plus (n0, n1) by row: w[8-key tile][row]
+        auto scores = [&](int h, f32x2 n0, f32x2 n1, f32x2 (&w)[4]) {
+          float s[2][4] = {};
+          tc_dot<KC>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-            const f32x2 x = at[0], y = at[kTcStage / 2], z = at[kTcStage];
+            w[2 * c] = f2_pack(s[c][0], s[c][1]);
+            w[2 * c + 1] = f2_pack(s[c][2], s[c][3]);
+          }
+          if constexpr (CAP) {
+            f32x2 none[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = f2_mul(w[i], c_in);
+            tc_cap<4, false>(w, none);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = f2_fma(w[i], CAP ? c_cap : c_in, (i & 1) ? n1 : n0);
+            if constexpr (BIAS) w[i] = f2_fma(d[i >> 1][i & 1], slope[h], w[i]);
+          }
+        };
+        f32x2 w[HP][4];
+        bool move = false;
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          scores(h, ref[h][0], ref[h][1], w[h]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float v[4];
+            f2_unpack(w[h][r], v[0], v[1]);
+            f2_unpack(w[h][2 + r], v[2], v[3]);
+            // all NaN without a reference
+            move |= !(fmaxf(tc_max3(v[0], v[1], v[2]), v[3]) <= 8.f);
+          }
+        }
+        auto mask = [&](int h) {   // keys past the molecule
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(w[h][i], a, b);
+            if (j + 8 * (i >> 1) + t2 >= n) a = -INFINITY;
+            if (j + 8 * (i >> 1) + t2 + 1 >= n) b = -INFINITY;
+            w[h][i] = f2_pack(a, b);
+          }
+        };
+        if (__any_sync(~0u, move)) {
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            scores(h, 0ull, 0ull, w[h]);
+            if (j + 16 > n) mask(h);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const f32x2 dx = f2_add(x, px[r]), dy = f2_add(y, py[r]), dz = f2_add(z, pz[r]);
-              float a, b;
-              f2_unpack(f2_fma(dx, dx, f2_fma(dy, dy, f2_mul(dz, dz))), a, b);
-              d[c][r] = f2_pack(mol_sqrt(a), mol_sqrt(b));
+              float v[4], old, unused1;
+              f2_unpack(w[h][r], v[0], v[1]);
+              f2_unpack(w[h][2 + r], v[2], v[3]);
+              f2_unpack(ref[h][r], old, unused1);
+              const float top = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+              const float up = fmaxf(-old, top);   // a NaN reference drops out
+              // all -inf so far: no reference, no weights
+              const bool none = up == -INFINITY;
+              const float f = none || isnan(old) ? 0.f : fast_exp2(-old - up);
+              ref[h][r] = f2_set(none ? __int_as_float(0x7fffffff) : -up);
+              sum[h][r] = f2_mul(sum[h][r], f2_set(f));
+#pragma unroll
+              for (int x = 0; x < NT; ++x) {
+                acc[h][x][2 * r] *= f;
+                acc[h][x][2 * r + 1] *= f;
+              }
+              const f32x2 shift = f2_set(none ? 0.f : -up);
+              w[h][r] = f2_add(w[h][r], shift);
+              w[h][2 + r] = f2_add(w[h][2 + r], shift);
             }
           }
+        } else if (j + 16 > n) {
+#pragma unroll
+          for (int h = 0; h < HP; ++h) mask(h);
         }
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          float s[2][4] = {};
-          tc_dot<KC>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
-          f32x2 x[2][2];   // scores in base 2, before the reference is taken off
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[c][0] = f2_pack(s[c][0], s[c][1]);
-            x[c][1] = f2_pack(s[c][2], s[c][3]);
-          }
-          if (capped) {
-            f32x2 unused;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              x[c][0] = f2_mul(x[c][0], c_in);
-              x[c][1] = f2_mul(x[c][1], c_in);
-              tc_cap<false>(x[c][0], x[c][1], unused, unused);
-            }
-          }
-          float w[2][4];
-          auto score = [&](float m0, float m1) {
-            const f32x2 cm = capped ? c_cap : c_in;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              f32x2 a = f2_fma(x[c][0], cm, f2_set(-m0)), b = f2_fma(x[c][1], cm, f2_set(-m1));
-              if (p.a.slope) {
-                a = f2_fma(d[c][0], slope[h], a);
-                b = f2_fma(d[c][1], slope[h], b);
-              }
-              f2_unpack(a, w[c][0], w[c][1]);
-              f2_unpack(b, w[c][2], w[c][3]);
-              if (j + 16 > n) {   // keys past the molecule
-                if (j + 8 * c + t2 >= n) w[c][0] = w[c][2] = -INFINITY;
-                if (j + 8 * c + t2 + 1 >= n) w[c][1] = w[c][3] = -INFINITY;
-              }
-            }
-          };
-          score(mx[h][0], mx[h][1]);
-          const float top0 = fmaxf(fmaxf(w[0][0], w[0][1]), fmaxf(w[1][0], w[1][1]));
-          const float top1 = fmaxf(fmaxf(w[0][2], w[0][3]), fmaxf(w[1][2], w[1][3]));
-          // a row without a finite reference yet takes this way too: its w may be NaN from inf - inf
-          if (__any_sync(~0u, !(top0 <= 8.f) || !(top1 <= 8.f) || fminf(mx[h][0], mx[h][1]) == -INFINITY)) {
-            score(0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float up = fmaxf(mx[h][r], quad_max(fmaxf(fmaxf(w[0][2 * r], w[0][2 * r + 1]),
-                                                              fmaxf(w[1][2 * r], w[1][2 * r + 1]))));
-              const float f = up == -INFINITY ? 1.f : fast_exp2(mx[h][r] - up);
-              const float ref = up == -INFINITY ? 0.f : up;
-              mx[h][r] = up;
-              sum[h][r] *= f;
-#pragma unroll
-              for (int x8 = 0; x8 < NT; ++x8) {
-                acc[h][x8][2 * r] *= f;
-                acc[h][x8][2 * r + 1] *= f;
-              }
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                w[c][2 * r] -= ref;
-                w[c][2 * r + 1] -= ref;
-              }
-            }
-          }
           uint32_t pf[2][2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float a = fast_exp2(w[c][2 * r]), b = fast_exp2(w[c][2 * r + 1]);
-              sum[h][r] += a + b;
-              pf[c][r] = tc_pack(a, b);
-            }
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(w[h][i], a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[h][i & 1] = f2_add(sum[h][i & 1], f2_pack(a, b));
+            pf[i >> 1][i & 1] = tc_pack(a, b);
+          }
           tc_apply<NT>(acc[h], pf, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16);
         }
       }
@@ -174,9 +184,12 @@ __global__ void __launch_bounds__(kTcThreads) mol_fwd_tc_kernel(MolParams p) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = warp * 16 + g + 8 * r;
-      const float l = quad_sum(sum[h][r]);
+      float lo, hi, mr;
+      f2_unpack(sum[h][r], lo, hi);
+      const float l = quad_sum(lo + hi);
+      f2_unpack(ref[h][r], mr, hi);
       if (t2 == 0) {
-        oml[(row * HP + h) * 2] = mx[h][r];
+        oml[(row * HP + h) * 2] = isnan(mr) ? -INFINITY : -mr;
         oml[(row * HP + h) * 2 + 1] = l;
       }
 #pragma unroll
@@ -242,7 +255,10 @@ int mol_tc_forward(const MolParams& p, cudaStream_t st) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP>;
     const size_t shm = std::max(2 * L::STAGE, 4 * 16 * (L::OUTROW + 2 * HP) * 4);
-    return tc_launch(mol_fwd_tc_kernel<NT, KC, HP>, dim3(p.slots, p.H / HP, p.splits), shm, p, st);
+    const dim3 grid(p.slots, p.H / HP, p.splits);
+    return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
+      return tc_launch(mol_fwd_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value>, grid, shm, p, st);
+    });
   });
 }
 

@@ -71,6 +71,15 @@ __device__ __forceinline__ void tc_mma16(float (&c)[4], const uint32_t (&a0)[2],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0[0]), "r"(a0[1]), "r"(a1[0]), "r"(a1[1]), "r"(b0), "r"(b1));
 }
+// c = a b
+__device__ __forceinline__ void tc_mma16_first(float (&c)[4], const uint32_t (&a0)[2], const uint32_t (&a1)[2],
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0[0]), "r"(a0[1]), "r"(a1[0]), "r"(a1[1]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void tc_mma8(float (&c)[4], const uint32_t (&a)[2], uint32_t b) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};\n"
@@ -85,6 +94,13 @@ __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+// max(a, b, c) in one instruction (the three-input form of sm_100); drops NaN
+// operands unless all are NaN
+__device__ __forceinline__ float tc_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ f32x2 f2_set(float x) { return f2_pack(x, x); }
 __device__ __forceinline__ float quad_sum(float x) {
@@ -101,33 +117,70 @@ __device__ __forceinline__ int tc_val_off(const MolParams& p, int h, int x) {
   return (x >> p.ch8log) * p.C + h * p.ch + ((x & ((1 << p.ch8log) - 1)) << 3);
 }
 
-// Rows [r0, r0 + 64) of heads head0.. into a stage; rows from `end` on as zeros.
-template <int NT, int KC, int HP>
-__device__ __forceinline__ void tc_load_stage(const MolParams& p, const __nv_bfloat16* qk, const __nv_bfloat16* val,
-                                              const float* pos, int head0, int r0, int end, uint32_t st) {
-  using L = TcLay<NT, KC, HP>;
-  const int kc = p.dk >> 3;   // below KC at dk 8: the second chunk is zeros
+// Copies consecutive stages of 64 rows of heads head0.. asynchronously.  A row's W
+// chunks are copied by W lanes, 32 / W rows at a time, so a lane keeps its chunk and
+// advances by whole rows.  Rows from `end` on arrive as zeros.
+template <int W>
+struct TcPart {
+  static_assert(W <= 32, "a row's chunks are one warp's");
+  static constexpr int ROWS = 32 / W, STEP = ROWS * (kTcThreads / 32), ITS = kTcStage / STEP;
+  const __nv_bfloat16* src;   // this lane's chunk of its first row
+  int ld;                     // elements from row to row
+  uint32_t dst;
+  int row;                    // its first row in a stage; past the stage: nothing to copy
+  __device__ __forceinline__ void init(const __nv_bfloat16* base, int ld_, int off, int r0, uint32_t at, int rs) {
+    const int lane = threadIdx.x & 31, r = (threadIdx.x >> 5) * ROWS + lane / W;
+    row = lane < ROWS * W ? r : kTcStage;
+    ld = ld_;
+    src = base + size_t(r0 + r) * ld + off;
+    dst = at + r * rs + (lane % W) * 16;
+  }
+  template <int RS>
+  __device__ __forceinline__ void load(uint32_t st, int left, bool have) {
+    if (row < kTcStage) {
+      if (left >= kTcStage && have) {
 #pragma unroll
-  for (int i = threadIdx.x; i < kTcStage * HP * KC; i += kTcThreads) {
-    const int r = i / (HP * KC), c = i % (HP * KC), hp = c / KC, cc = c % KC;
-    const bool ok = r0 + r < end && cc < kc;
-    tc_cp16(st + L::QK + r * L::RK + c * 16,
-            ok ? qk + (size_t(r0 + r) * p.H + head0 + hp) * p.dk + cc * 8 : qk, ok);
-  }
-#pragma unroll 4
-  for (int i = threadIdx.x; i < kTcStage * HP * NT; i += kTcThreads) {
-    const int r = i / (HP * NT), c = i % (HP * NT), x = c / HP, hp = c % HP;
-    const bool ok = r0 + r < end;
-    tc_cp16(st + L::VAL + r * L::RV + c * 16,
-            ok ? val + size_t(r0 + r) * (p.D * p.C) + tc_val_off(p, head0 + hp, x) : val, ok);
-  }
-  if (p.a.slope)
-    for (int i = threadIdx.x; i < 3 * kTcStage; i += kTcThreads) {
-      const int r = i / 3, c = i % 3;
-      const bool ok = r0 + r < end;
-      tc_cp4(st + L::POS + c * (kTcStage * 4) + r * 4, ok ? pos + size_t(r0) * 3 + i : pos, ok);
+        for (int i = 0; i < ITS; ++i) tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < ITS; ++i) {
+          const bool ok = have && row + i * STEP < left;
+          tc_cp16(st + dst + i * STEP * RS, ok ? src + size_t(i) * STEP * ld : src - size_t(row) * ld, ok);
+        }
+      }
     }
-}
+    src += size_t(kTcStage) * ld;
+  }
+};
+template <int NT, int KC, int HP>
+struct TcLoader {
+  using L = TcLay<NT, KC, HP>;
+  TcPart<HP * KC> qk;
+  TcPart<HP * NT> val;
+  const float* pos;
+  bool have;   // at dk 8 the second chunk is zeros
+  // the first stage starts at row r0 (r0 < end)
+  __device__ __forceinline__ void init(const MolParams& p, const __nv_bfloat16* q, const __nv_bfloat16* v,
+                                       const float* positions, int head0, int r0) {
+    const int lane = threadIdx.x & 31, cq = lane % (HP * KC), cv = lane % (HP * NT);
+    have = (cq % KC) * 8 < p.dk;
+    qk.init(q, p.H * p.dk, (head0 + cq / KC) * p.dk + (have ? cq % KC : 0) * 8, r0, L::QK, L::RK);
+    val.init(v, p.D * p.C, tc_val_off(p, head0 + cv % HP, cv / HP), r0, L::VAL, L::RV);
+    pos = p.a.slope ? positions + size_t(r0) * 3 : nullptr;
+  }
+  __device__ __forceinline__ void load(uint32_t st, int left) {
+    qk.template load<L::RK>(st, left, have);
+    val.template load<L::RV>(st, left, true);
+    if (pos) {
+      const int c = threadIdx.x >> 5;
+      if (c < 3)
+#pragma unroll
+        for (int r = threadIdx.x & 31; r < kTcStage; r += 32)
+          tc_cp4(st + L::POS + c * (kTcStage * 4) + r * 4, r < left ? pos + r * 3 + c : pos, r < left);
+      pos += kTcStage * 3;
+    }
+  }
+};
 
 // A fragments of this lane's rows (r0 = row g, r1 = row g + 8) from global memory
 template <int KC>
@@ -152,19 +205,34 @@ __device__ __forceinline__ void tc_frag_val(const MolParams& p, const __nv_bfloa
   }
 }
 
-// acc[16 rows x 16 other rows] = A (16 rows x NC chunks) . (other rows)^T:
+// acc (16 rows x 16 other rows) = (or, with ADD, +=) A (16 rows x NC chunks) . (other rows)^T:
 // base is the lane's address of chunk 0 for a non-transposed x4 load (rows by
 // lane & 7 and lane / 16, chunk by bit 3), base2 that of an x2 load of a last odd
 // chunk; step: bytes from a chunk to the next.
-template <int NC>
+template <int NC, bool ADD = false>
 __device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[NC][2], uint32_t base, uint32_t base2,
                                        int step) {
+  static_assert(NC > 1 || !ADD, "");
+  if constexpr (NC == 1) {
+    uint32_t b0, b1;
+    tc_ldsm2(base2, b0, b1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.f;
+    tc_mma8(acc[0], a[0], b0);
+    tc_mma8(acc[1], a[0], b1);
+    return;
+  }
 #pragma unroll
   for (int c = 0; c + 1 < NC; c += 2) {
     uint32_t b[4];
     tc_ldsm4(base + c * step, b);
-    tc_mma16(acc[0], a[c], a[c + 1], b[0], b[1]);
-    tc_mma16(acc[1], a[c], a[c + 1], b[2], b[3]);
+    if (c == 0 && !ADD) {
+      tc_mma16_first(acc[0], a[c], a[c + 1], b[0], b[1]);
+      tc_mma16_first(acc[1], a[c], a[c + 1], b[2], b[3]);
+    } else {
+      tc_mma16(acc[0], a[c], a[c + 1], b[0], b[1]);
+      tc_mma16(acc[1], a[c], a[c + 1], b[2], b[3]);
+    }
   }
   if constexpr (NC & 1) {
     uint32_t b0, b1;
@@ -215,31 +283,32 @@ __device__ __forceinline__ f32x2 tc_tanh_small(f32x2 x) {
   r = f2_fma(z, r, f2_set(9.999999502e-01f));
   return f2_mul(x, r);
 }
-// x = cap tanh of 4 logits (an accumulator fragment), in units of 1 / cap, and f' if wanted
-template <bool WANT>
-__device__ __forceinline__ void tc_cap(f32x2& a, f32x2& b, f32x2& fa, f32x2& fb) {
-  float v[4];
-  f2_unpack(a, v[0], v[1]);
-  f2_unpack(b, v[2], v[3]);
-  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-  if (!(top <= 1.f)) {
-    float d[4];
+// tanh of a step's logits (units of the cap) in place, and the derivative if wanted
+template <int N, bool WANT>
+__device__ __forceinline__ void tc_cap(f32x2 (&x)[N], f32x2 (&fx)[WANT ? N : 1]) {
+  float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mol_tanh(v[i], d[i]);
-    a = f2_pack(v[0], v[1]);
-    b = f2_pack(v[2], v[3]);
-    if (WANT) {
-      fa = f2_pack(d[0], d[1]);
-      fb = f2_pack(d[2], d[3]);
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    f2_unpack(x[i], a, b);
+    top = tc_max3(top, fabsf(a), fabsf(b));
+  }
+  if (top > 1.f) {   // a NaN logit stays NaN either way
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float a, b, da, db;
+      f2_unpack(x[i], a, b);
+      a = mol_tanh(a, da);
+      b = mol_tanh(b, db);
+      x[i] = f2_pack(a, b);
+      if (WANT) fx[i] = f2_pack(da, db);
     }
     return;
   }
-  a = tc_tanh_small(a);
-  b = tc_tanh_small(b);
-  if (WANT) {
-    const f32x2 one = f2_set(1.f);
-    fa = f2_fma(f2_mul(a, f2_set(-1.f)), a, one);
-    fb = f2_fma(f2_mul(b, f2_set(-1.f)), b, one);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = tc_tanh_small(x[i]);
+    if (WANT) fx[i] = f2_fma(f2_mul(x[i], f2_set(-1.f)), x[i], f2_set(1.f));
   }
 }
 
@@ -251,9 +320,30 @@ __device__ __forceinline__ void tc_dist(float a, float b, f32x2& d, f32x2& ri) {
     d = f2_pack(mol_sqrt(a), mol_sqrt(b));
     return;
   }
-  const float ra = rsqrtf(fminf(fmaxf(a, 1e-37f), 3.4e38f)), rb = rsqrtf(fminf(fmaxf(b, 1e-37f), 3.4e38f));
+  float ra, rb;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(fminf(fmaxf(a, 1e-37f), 3.4e38f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(fminf(fmaxf(b, 1e-37f), 3.4e38f)));
   ri = f2_pack(ra, rb);
   d = f2_mul(f2_pack(a, b), ri);   // NaN and inf of the squares stay
+}
+
+// Distances of this lane's two rows (px.. = minus their positions) to the keys
+// 2t, 2t + 1 of both 8-key tiles at sp: [tile][row], and with RECIP their reciprocals
+template <bool RECIP>
+__device__ __forceinline__ void tc_dists(const float* sp, const f32x2 (&px)[2], const f32x2 (&py)[2],
+                                         const f32x2 (&pz)[2], f32x2 (&d)[2][2], f32x2 (&ri)[2][2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const f32x2* at = reinterpret_cast<const f32x2*>(sp + 8 * c);
+    const f32x2 x = at[0], y = at[kTcStage / 2], z = at[kTcStage];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const f32x2 dx = f2_add(x, px[r]), dy = f2_add(y, py[r]), dz = f2_add(z, pz[r]);
+      float a, b;
+      f2_unpack(f2_fma(dx, dx, f2_fma(dy, dy, f2_mul(dz, dz))), a, b);
+      tc_dist<RECIP>(a, b, d[c][r], ri[c][r]);
+    }
+  }
 }
 
 // Calls f with the value tiles, the query chunks and the heads of a warp.
@@ -277,6 +367,13 @@ int tc_dispatch(int nt, int dk, F&& f) {
     default: return EGAT_ERR_UNSUPPORTED;
   }
 #undef EGAT_TC
+}
+
+// ... and f with two flags
+template <typename F>
+int mol_flags(bool a, bool b, F&& f) {
+  if (a) return b ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  return b ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
 }
 
 template <typename K>
