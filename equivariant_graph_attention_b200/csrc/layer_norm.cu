@@ -113,34 +113,66 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-template <int E>
+// E float32 parameters; VEC: their pointer is 16-byte aligned
+template <int E, bool VEC>
 __device__ __forceinline__ void load_f32(const float* p, int c, float dflt, float (&o)[E]) {
   if (!p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = dflt;
     return;
   }
-  // float32 parameters need no more than their own alignment
+  if constexpr (VEC && E == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c) + 1);
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+  } else {
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = __ldg(p + c + e);
+    for (int e = 0; e < E; ++e) o[e] = __ldg(p + c + e);
+  }
 }
+
+// A thread keeps its columns' parameters over the rows that it visits where they
+// fit its registers, and reads them again for every row otherwise.
+template <int E, int V>
+constexpr bool norm_hold() { return E == 8 && V <= 4; }
 
 template <typename T, int E, int TPR, int V>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(NormParams p) {
   constexpr int NT = norm_threads<TPR>();
+  constexpr bool HOLD = norm_hold<E, V>();
   __shared__ float red[32];
   const int lane = threadIdx.x % TPR;
   const long long stride = (long long)gridDim.x * (NT / TPR);
-  // whole blocks stay in step: row_sum shuffles and, for TPR > 32, synchronises
-  for (long long r0 = (long long)blockIdx.x * (NT / TPR); r0 < p.n; r0 += stride) {
-    const long long row = r0 + threadIdx.x / TPR;
-    const bool live = row < p.n;
-    const T* x = static_cast<const T*>(p.x) + (live ? row : r0) * p.ldx;
-    Vec<T, E> raw[V];
+  float hw[HOLD ? V : 1][E], hb[HOLD ? V : 1][E];
+  if constexpr (HOLD) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (lane + i * TPR) * E;
-      if (c < p.width) raw[i].load(x + c);
+      if (c < p.width) {
+        load_f32<E, true>(p.w, c, 1.f, hw[i]);
+        load_f32<E, true>(p.b, c, 0.f, hb[i]);
+      }
+    }
+  }
+  Vec<T, E> raw[V], next[HOLD ? V : 1];
+  auto fetch = [&](long long r0, Vec<T, E>(&v)[V]) {
+    const long long row = r0 + threadIdx.x / TPR;
+    const T* x = static_cast<const T*>(p.x) + (row < p.n ? row : r0) * p.ldx;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (lane + i * TPR) * E;
+      if (c < p.width) v[i].load(x + c);
+    }
+  };
+  // whole blocks stay in step: row_sum shuffles and, for TPR > 32, synchronises
+  long long r0 = (long long)blockIdx.x * (NT / TPR);
+  if (HOLD && r0 < p.n) fetch(r0, raw);
+  for (; r0 < p.n; r0 += stride) {
+    const long long row = r0 + threadIdx.x / TPR;
+    const bool live = row < p.n;
+    if constexpr (HOLD) {
+      if (r0 + stride < p.n) fetch(r0 + stride, next);   // the next row is on its way meanwhile
+    } else {
+      fetch(r0, raw);
     }
     float s = 0.f;
 #pragma unroll
@@ -162,24 +194,34 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(NormParam
         for (int e = 0; e < E; ++e) s = fmaf(v[e] - mu, v[e] - mu, s);
       }
     const float rstd = rsqrtf(row_sum<TPR>(s, red) * p.inv_width + p.eps);
-    if (!live) continue;
-    T* y = static_cast<T*>(p.y) + row * p.ldy;
+    if (live) {
+      T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (lane + i * TPR) * E;
-      if (c < p.width) {
-        float v[E], w[E], b[E];
-        raw[i].get(v);
-        load_f32(p.w, c, 1.f, w);
-        load_f32(p.b, c, 0.f, b);
+      for (int i = 0; i < V; ++i) {
+        const int c = (lane + i * TPR) * E;
+        if (c < p.width) {
+          float v[E], w[E], b[E];
+          raw[i].get(v);
+          if constexpr (HOLD) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mu) * rstd, w[e], b[e]);
-        Vec<T, E>::store(y + c, v);
+            for (int e = 0; e < E; ++e) w[e] = hw[i][e], b[e] = hb[i][e];
+          } else {
+            load_f32<E, false>(p.w, c, 1.f, w);
+            load_f32<E, false>(p.b, c, 0.f, b);
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mu) * rstd, w[e], b[e]);
+          Vec<T, E>::store(y + c, v);
+        }
+      }
+      if (lane == 0 && p.stats_out) {
+        p.stats_out[2 * row] = mu;
+        p.stats_out[2 * row + 1] = rstd;
       }
     }
-    if (lane == 0 && p.stats_out) {
-      p.stats_out[2 * row] = mu;
-      p.stats_out[2 * row + 1] = rstd;
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) raw[i] = next[i];
     }
   }
 }
@@ -187,10 +229,16 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(NormParam
 template <typename T, int E, int TPR, int V>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParams p) {
   constexpr int NT = norm_threads<TPR>(), WARPS = NT / 32;
+  constexpr bool HOLD = norm_hold<E, V>();
   extern __shared__ float sums[];   // [2][width]
   __shared__ float red[32];
   const int lane = threadIdx.x % TPR;
-  float dw[V][E] = {}, db[V][E] = {};
+  float dw[V][E] = {}, db[V][E] = {}, hw[HOLD ? V : 1][E];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((lane + i * TPR) * E < p.width) load_f32<E, true>(p.w, (lane + i * TPR) * E, 1.f, hw[i]);
+  }
   const long long stride = (long long)gridDim.x * (NT / TPR);
   for (long long r0 = (long long)blockIdx.x * (NT / TPR); r0 < p.n; r0 += stride) {
     const long long row = r0 + threadIdx.x / TPR;
@@ -208,6 +256,14 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
       }
     }
     const float mu = p.stats[2 * at], rstd = p.stats[2 * at + 1];
+    auto weight = [&](int i, float (&w)[E]) {
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = hw[i][e];
+      } else {
+        load_f32<E, false>(p.w, (lane + i * TPR) * E, 1.f, w);
+      }
+    };
     float st = 0.f, sx = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -216,7 +272,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
         float xv[E], gv[E], w[E];
         rx[i].get(xv);
         rg[i].get(gv);
-        load_f32(p.w, c, 1.f, w);
+        weight(i, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float xh = (xv[e] - mu) * rstd, t = gv[e] * w[e];
@@ -241,7 +297,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
         float xv[E], gv[E], w[E];
         rx[i].get(xv);
         rg[i].get(gv);
-        load_f32(p.w, c, 1.f, w);
+        weight(i, w);
 #pragma unroll
         for (int e = 0; e < E; ++e)
           xv[e] = rstd * (gv[e] * w[e] - mt - (xv[e] - mu) * rstd * mx);
@@ -293,21 +349,28 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
   }
 }
 
-// Adds the partial rows: 32 columns a block, 8 threads down each column.
-__global__ void norm_reduce_kernel(const float* part, int blocks, int width, float* dw, float* db) {
-  __shared__ float sm[8][33];
+// Adds the partial rows: 32 columns a block, 32 threads down each column with
+// four sums each, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int blocks, int width, float* dw, float* db) {
+  __shared__ float sm[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
-  float s = 0.f;
-  if (c < 2 * width)
-    for (int b = threadIdx.y; b < blocks; b += 8) s += part[size_t(b) * 2 * width + c];
-  sm[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < 2 * width) {
-    s = 0.f;
+  float s[4] = {};
+  if (c < 2 * width) {
+    int b = threadIdx.y;
+    for (; b + 96 < blocks; b += 128)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += sm[i][threadIdx.x];
-    float* out = c < width ? dw : db;
-    if (out) out[c < width ? c : c - width] = s;
+      for (int i = 0; i < 4; ++i) s[i] += part[size_t(b + 32 * i) * 2 * width + c];
+    for (; b < blocks; b += 32) s[0] += part[size_t(b) * 2 * width + c];
+  }
+  sm[threadIdx.y][threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  float v = sm[threadIdx.x][threadIdx.y];   // a warp adds one column
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  const int col = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && col < 2 * width) {
+    float* out = col < width ? dw : db;
+    if (out) out[col < width ? col : col - width] = v;
   }
 }
 
@@ -343,15 +406,16 @@ int by_width_e(int width, F&& f) {
 // The widest vectors that width, strides and pointers allow: 16-byte vectors
 // of bf16 or 16-byte halves of float32, pairs, or elements.
 template <typename T, typename F>
-int by_width(int width, const void* a, long long lda, const void* b, long long ldb, const void* c,
-             long long ldc, F&& f) {
+int by_width(int width, const float* w, const float* bias, const void* a, long long lda, const void* b,
+             long long ldb, const void* c, long long ldc, F&& f) {
   auto fits = [&](int e, size_t bytes) {
     auto one = [&](const void* q, long long ld) {
       return !q || (reinterpret_cast<uintptr_t>(q) % bytes == 0 && ld * (long long)sizeof(T) % (long long)bytes == 0);
     };
     return width % e == 0 && one(a, lda) && one(b, ldb) && one(c, ldc);
   };
-  if (fits(8, 16)) return by_width_e<8>(width, f);
+  const bool params = ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
+  if (fits(8, 16) && params) return by_width_e<8>(width, f);
   if (fits(2, 2 * sizeof(T))) return by_width_e<2>(width, f);
   return by_width_e<1>(width, f);
 }
@@ -360,10 +424,12 @@ int launched() { return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_C
 
 template <typename T>
 int norm_fwd_t(const NormParams& p, cudaStream_t st) {
-  return by_width<T>(p.width, p.x, p.ldx, p.y, p.ldy, nullptr, 0, [&](auto e, auto tpr, auto v) {
+  return by_width<T>(p.width, p.w, p.b, p.x, p.ldx, p.y, p.ldy, nullptr, 0, [&](auto e, auto tpr, auto v) {
     constexpr int E = decltype(e)::value, TPR = decltype(tpr)::value, V = decltype(v)::value;
     constexpr int NT = norm_threads<TPR>(), ROWS = NT / TPR;
-    const long long blocks = ((long long)p.n + ROWS - 1) / ROWS;
+    // up to eight blocks an SM; beyond, a block takes several rows with its
+    // parameters in registers and the next row on its way
+    const long long blocks = std::min<long long>(148 * 8, ((long long)p.n + ROWS - 1) / ROWS);
     norm_fwd_kernel<T, E, TPR, V><<<unsigned(blocks), NT, 0, st>>>(p);
     return launched();
   });
@@ -378,7 +444,7 @@ int norm_blocks(int n, int rows_per_block) {
 template <typename T>
 int norm_bwd_t(NormParams p, bool want_w, float* d_dw, float* d_db, cudaStream_t st) {
   int blocks = 0;
-  const int rc = by_width<T>(p.width, p.x, p.ldx, p.y, p.ldy, p.g, p.ldg, [&](auto e, auto tpr, auto v) {
+  const int rc = by_width<T>(p.width, p.w, p.b, p.x, p.ldx, p.y, p.ldy, p.g, p.ldg, [&](auto e, auto tpr, auto v) {
     constexpr int E = decltype(e)::value, TPR = decltype(tpr)::value, V = decltype(v)::value;
     constexpr int NT = norm_threads<TPR>(), ROWS = NT / TPR;
     blocks = norm_blocks(p.n, ROWS);
@@ -387,7 +453,7 @@ int norm_bwd_t(NormParams p, bool want_w, float* d_dw, float* d_db, cudaStream_t
     return launched();
   });
   if (rc != EGAT_OK || !want_w) return rc;
-  norm_reduce_kernel<<<(2 * p.width + 31) / 32, dim3(32, 8), 0, st>>>(p.part, blocks, p.width, d_dw, d_db);
+  norm_reduce_kernel<<<(2 * p.width + 31) / 32, dim3(32, 32), 0, st>>>(p.part, blocks, p.width, d_dw, d_db);
   return launched();
 }
 

@@ -12,6 +12,7 @@ Function names match the C entry points (``egat_build_graph`` ...).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -533,38 +534,72 @@ def _typed(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Option
     """The pointer of a contiguous tensor of this type, shape and device; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"egat: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"egat: {name} is on {t.device}, not on {device}")
-    return _ptr(t)
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"egat: {name} must live on the CUDA device {device}, not on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"egat: {name} must be contiguous")
+    return t.data_ptr()
 
 
-def _scratch(nb: int, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+class _on:
+    """The device of a call's tensors as the current one; free where it is already."""
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError("egat: tensors must live on a CUDA device")
+        self.device, self.guard = device, None
+
+    def __enter__(self):
+        if torch._C._cuda_getDevice() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _stream_of(stream, device: torch.device) -> int:
+    """The given stream, or the device's current one, as an integer handle."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _scratch(nb: int, workspace: Optional[torch.Tensor], device):
+    """The workspace of a call and its size in bytes: the caller's, or a new one if one is needed."""
     if workspace is None:
-        return torch.empty(max(nb, 16), dtype=torch.uint8, device=device)
-    if workspace.device != device:
-        raise ValueError(f"egat: workspace is on {workspace.device}, not on {device}")
-    return workspace
+        return (torch.empty(nb, dtype=torch.uint8, device=device), nb) if nb else (None, 0)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"egat: workspace must be contiguous on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _mol_inputs(s: MoleculeShape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev):
     T = s.torch_dtype
-    return [_typed("q", q, T, (s.nq, s.H, s.dk), dev), _typed("k", k, T, (s.nk, s.H, s.dk), dev),
+    return (_typed("q", q, T, (s.nq, s.H, s.dk), dev), _typed("k", k, T, (s.nk, s.H, s.dk), dev),
             _typed("hp", hp, T, (s.nk, s.D, s.C), dev),
             _typed("q_ptr", q_ptr, torch.int32, (s.n_mol + 1,), dev),
             _typed("k_ptr", k_ptr, torch.int32, (s.n_mol + 1,), dev),
             _typed("pos_q", pos_q, torch.float32, (s.nq, 3), dev),
             _typed("pos_k", pos_k, torch.float32, (s.nk, 3), dev),
-            _typed("slope", slope, torch.float32, (s.H,), dev)]
+            _typed("slope", slope, torch.float32, (s.H,), dev))
+
+
+@functools.lru_cache(maxsize=256)
+def _mol_call(shape: MoleculeShape):
+    """The shape as the library takes it, and the forward's and the backward's workspace sizes."""
+    cs, out = shape.c(), ctypes.c_size_t(0)
+    sizes = []
+    for name in ("egat_molecule_attention_workspace_bytes", "egat_molecule_attention_backward_workspace_bytes"):
+        _check(name, getattr(load_library(), name)(ctypes.byref(cs), ctypes.byref(out)))
+        sizes.append(out.value)
+    return ctypes.byref(cs), sizes[0], sizes[1]
 
 
 def egat_molecule_attention_workspace_bytes(shape: MoleculeShape) -> int:
-    out = ctypes.c_size_t(0)
-    cs = shape.c()
-    _check("egat_molecule_attention_workspace_bytes",
-           load_library().egat_molecule_attention_workspace_bytes(ctypes.byref(cs), ctypes.byref(out)))
-    return out.value
+    return _mol_call(shape)[1]
 
 
 def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tensor,
@@ -582,27 +617,23 @@ def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tens
     device; k_ptr None: the queries' own atoms).  Returns (m [nq, D, C] in the storage type,
     lse float32 [nq, H] or None); rows without keys get 0 and -inf."""
     dev = q.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+        cs, nb, _ = _mol_call(shape)
+        vals = (shape.nq, shape.D, shape.C)
         if out is None:
-            out = torch.empty((shape.nq, shape.D, shape.C), dtype=shape.torch_dtype, device=dev)
-        po = _typed("out", out, shape.torch_dtype, (shape.nq, shape.D, shape.C), dev)
+            out = torch.empty(vals, dtype=shape.torch_dtype, device=dev)
+        po = _typed("out", out, shape.torch_dtype, vals, dev)
         lse = torch.empty((shape.nq, shape.H), dtype=torch.float32, device=dev) if want_lse else None
-        ws = _scratch(egat_molecule_attention_workspace_bytes(shape), workspace, dev)
-        cs = shape.c()
-        rc = load_library().egat_molecule_attention(ctypes.byref(cs), *ptrs, _ptr(ws), ws.numel(), po,
-                                                    _ptr(lse), _stream(stream))
+        ws, nb = _scratch(nb, workspace, dev)
+        rc = load_library().egat_molecule_attention(cs, *ptrs, None if ws is None else ws.data_ptr(), nb, po,
+                                                    None if lse is None else lse.data_ptr(), _stream_of(stream, dev))
     _check("egat_molecule_attention", rc)
     return out, lse
 
 
 def egat_molecule_attention_backward_workspace_bytes(shape: MoleculeShape) -> int:
-    out = ctypes.c_size_t(0)
-    cs = shape.c()
-    _check("egat_molecule_attention_backward_workspace_bytes",
-           load_library().egat_molecule_attention_backward_workspace_bytes(ctypes.byref(cs),
-                                                                           ctypes.byref(out)))
-    return out.value
+    return _mol_call(shape)[2]
 
 
 def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: torch.Tensor,
@@ -618,37 +649,40 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
     whole dL/dr and dpos_k is None; without a slope, or with positions=False (cheaper), the
     last three are None."""
     dev, T = q.device, shape.torch_dtype
-    with torch.cuda.device(dev):
+    with _on(dev):
         ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+        cs, _, nb = _mol_call(shape)
         vals = (shape.nq, shape.D, shape.C)
-        ptrs += [_typed("m", m, T, vals, dev), _typed("lse", lse, torch.float32, (shape.nq, shape.H), dev),
-                 _typed("grad_m", grad_m, T, vals, dev)]
-        ws = _scratch(egat_molecule_attention_backward_workspace_bytes(shape), workspace, dev)
+        pm, pl, pg = (_typed("m", m, T, vals, dev), _typed("lse", lse, torch.float32, (shape.nq, shape.H), dev),
+                      _typed("grad_m", grad_m, T, vals, dev))
+        ws, nb = _scratch(nb, workspace, dev)
         dq, dk, dhp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(hp)
         dpos_q = dpos_k = dslope = None
         if slope is not None and positions:
             dpos_q, dslope = torch.empty_like(pos_q), torch.empty_like(slope)
             dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
-        cs = shape.c()
-        rc = load_library().egat_molecule_attention_backward(
-            ctypes.byref(cs), *ptrs, _ptr(ws), ws.numel(), _ptr(dq), _ptr(dk), _ptr(dhp), _ptr(dpos_q),
-            _ptr(dpos_k), _ptr(dslope), _stream(stream))
+        at = [None if t is None else t.data_ptr() for t in (ws, dq, dk, dhp, dpos_q, dpos_k, dslope)]
+        rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
+                                                             _stream_of(stream, dev))
     _check("egat_molecule_attention_backward", rc)
     return dq, dk, dhp, dpos_q, dpos_k, dslope
 
 
-def _norm_rows(name: str, t: torch.Tensor, dtype, n: int, width: int, device):
+def _norm_rows(name: str, t: torch.Tensor, dtype, shape, device):
     """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype != dtype or tuple(t.shape) != (n, width):
-        raise ValueError(f"egat: {name} must be {dtype} [{n}, {width}], got {t.dtype} {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"egat: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda or t.device != device:
         raise ValueError(f"egat: {name} must live on the CUDA device {device}")
-    if width > 1 and t.stride(1) != 1:
+    n, width = shape
+    ld, one = t.stride()
+    if width > 1 and one != 1:
         raise ValueError(f"egat: {name} must have contiguous rows")
-    ld = t.stride(0) if n > 1 else width
+    if n <= 1:
+        return (t.data_ptr() if n else None), width
     if ld < width:
         raise ValueError(f"egat: rows of {name} overlap")
-    return t.data_ptr() if n > 0 else None, ld
+    return t.data_ptr(), ld
 
 
 def _norm_dtype(x: torch.Tensor) -> int:
@@ -663,26 +697,32 @@ def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     """Layer norm of the rows of x [n, width] (float32 or bf16; any row stride, so h[:, 0, :]
     works in place), weight and bias float32 [width].  Returns (y, stats float32 [n, 2] = mean
     and 1/std, or None).  out may be x itself."""
-    dt, (n, width), dev = _norm_dtype(x), x.shape, x.device
-    with torch.cuda.device(dev):
-        px, ldx = _norm_rows("x", x, x.dtype, n, width, dev)
+    dt, shape, dev, T = _norm_dtype(x), x.shape, x.device, x.dtype
+    n, width = shape
+    with _on(dev):
+        px, ldx = _norm_rows("x", x, T, shape, dev)
         pw = _typed("weight", weight, torch.float32, (width,), dev)
         pb = _typed("bias", bias, torch.float32, (width,), dev)
         if out is None:
-            out = torch.empty((n, width), dtype=x.dtype, device=dev)
-        py, ldy = _norm_rows("out", out, x.dtype, n, width, dev)
+            out = torch.empty(shape, dtype=T, device=dev)
+        py, ldy = _norm_rows("out", out, T, shape, dev)
         stats = torch.empty((n, 2), dtype=torch.float32, device=dev) if want_stats else None
-        rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy, _ptr(stats),
-                                            _stream(stream))
+        rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy,
+                                            None if stats is None else stats.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm", rc)
     return out, stats
 
 
-def egat_layer_norm_backward_workspace_bytes(n: int, width: int) -> int:
+@functools.lru_cache(maxsize=256)
+def _norm_ws(n: int, width: int) -> int:
     out = ctypes.c_size_t(0)
     _check("egat_layer_norm_backward_workspace_bytes",
            load_library().egat_layer_norm_backward_workspace_bytes(n, width, ctypes.byref(out)))
     return out.value
+
+
+def egat_layer_norm_backward_workspace_bytes(n: int, width: int) -> int:
+    return _norm_ws(n, width)
 
 
 def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], stats: torch.Tensor,
@@ -690,20 +730,21 @@ def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], st
                              workspace: Optional[torch.Tensor] = None, stream=None):
     """(dx in x's type, dweight, dbias float32 [width]) of the layer norm for the upstream
     gradient grad_y; stats as returned by the forward.  out (any row stride) receives dx."""
-    dt, (n, width), dev = _norm_dtype(x), x.shape, x.device
-    with torch.cuda.device(dev):
-        px, ldx = _norm_rows("x", x, x.dtype, n, width, dev)
-        pg, ldg = _norm_rows("grad_y", grad_y, x.dtype, n, width, dev)
+    dt, shape, dev, T = _norm_dtype(x), x.shape, x.device, x.dtype
+    n, width = shape
+    with _on(dev):
+        px, ldx = _norm_rows("x", x, T, shape, dev)
+        pg, ldg = _norm_rows("grad_y", grad_y, T, shape, dev)
         pw = _typed("weight", weight, torch.float32, (width,), dev)
         ps = _typed("stats", stats, torch.float32, (n, 2), dev)
         if out is None:
-            out = torch.empty((n, width), dtype=x.dtype, device=dev)
-        po, ldo = _norm_rows("out", out, x.dtype, n, width, dev)
+            out = torch.empty(shape, dtype=T, device=dev)
+        po, ldo = _norm_rows("out", out, T, shape, dev)
         dw = torch.empty(width, dtype=torch.float32, device=dev)
         db = torch.empty(width, dtype=torch.float32, device=dev)
-        ws = _scratch(egat_layer_norm_backward_workspace_bytes(n, width), workspace, dev)
-        rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg, _ptr(ws),
-                                                     ws.numel(), po, ldo, _ptr(dw), _ptr(db),
-                                                     _stream(stream))
+        ws, nb = _scratch(_norm_ws(n, width), workspace, dev)
+        rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg,
+                                                     None if ws is None else ws.data_ptr(), nb, po, ldo,
+                                                     dw.data_ptr(), db.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm_backward", rc)
     return out, dw, db
