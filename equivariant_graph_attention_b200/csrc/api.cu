@@ -251,16 +251,18 @@ int egat_forward(const egat_shape* s, const void* d_h, const float* d_pos, const
 
 int egat_take_device_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int a = 0, b = 0, c = 0, d = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, e = 0;
   const int ra = take_wait_timeouts_attention(st, &a);
   const int rb = take_wait_timeouts_coupling(st, &b);
   const int rc = take_wait_timeouts_backward(st, &c);
   const int rd = take_wait_timeouts_projection(st, &d);
+  const int re = take_wait_timeouts_molecule(st, &e);
   if (ra != EGAT_OK) return ra;
   if (rb != EGAT_OK) return rb;
   if (rc != EGAT_OK) return rc;
   if (rd != EGAT_OK) return rd;
-  return (a | b | c | d) ? EGAT_ERR_TIMEOUT : EGAT_OK;
+  if (re != EGAT_OK) return re;
+  return (a | b | c | d | e) ? EGAT_ERR_TIMEOUT : EGAT_OK;
 }
 
 int egat_qk_projection(const egat_shape* s, const void* d_h, const float* d_wq, const float* d_wk,

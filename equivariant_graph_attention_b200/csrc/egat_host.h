@@ -166,6 +166,7 @@ struct MolGrads {
   void *dq, *dk, *dhp;
   float *dposq, *dposk, *dslope;
 };
+int take_wait_timeouts_molecule(cudaStream_t st, unsigned int* count);
 size_t molecule_ws_bytes(const egat_mol_shape& s);
 int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d_ws, void* d_m,
                               float* d_lse, cudaStream_t st);

@@ -568,6 +568,7 @@ int generic_rows(const egat_mol_shape& s) {
 // the shape alone.
 struct MolCut {
   bool tc;
+  int umma;     // groups of 128 rows of the tcgen05 kernel, 0: not taken
   int rwlog;    // tensor-core tiles: 16 << rwlog rows
   int rows;     // rows of a tile
   int groups;   // blocks side by side over heads
@@ -585,15 +586,30 @@ int tc_rwlog(int n, int n_mol, int groups) {
     --l;
   return l;
 }
-MolCut forward_cut(const egat_mol_shape& s) {
+MolCut tile_cut(const egat_mol_shape& s) {
   MolCut c{};
   c.tc = mol_tc_supported(s);
   c.groups = c.tc ? s.H / mol_tc_heads(s) : s.H;
   c.rwlog = c.tc ? tc_rwlog(s.nq, s.n_mol, c.groups) : 0;
   c.rows = c.tc ? 16 << c.rwlog : generic_rows(s);
+  c.splits = 1;
+  return c;
+}
+MolCut forward_cut(const egat_mol_shape& s) {
+  MolCut c = tile_cut(s);
+  // Long molecules: tcgen05 tiles of 256 rows, or of 128 where those would leave
+  // SMs idle.
+  if (mol_umma_supported(s) && (long long)s.nq >= 192LL * s.n_mol && s.n_mol > 0 && s.nk >= 192LL * s.n_mol) {
+    const long long tiles = tile_blocks(s.nq, s.n_mol, 128, s.H);
+    if (tiles >= 148) {
+      c.umma = tiles >= 8 * 148 ? 2 : 1;
+      c.rows = 128 * c.umma;
+      c.splits = 1;
+      return c;
+    }
+  }
   // With fewer row tiles than four waves of 148 SMs, each molecule's keys are cut
   // so that about that many blocks run, but not below 128 keys a part on average.
-  c.splits = 1;
   if (s.n_mol > 0 && s.nk > 0 && c.rwlog == 0) {
     const long long blocks = std::max(1LL, tile_blocks(s.nq, s.n_mol, c.rows, c.groups));
     const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
@@ -661,7 +677,7 @@ struct MolBwdWs {
 };
 MolBwdWs bwd_ws(const egat_mol_shape& s) {
   MolBwdWs w;
-  w.cut = forward_cut(s);
+  w.cut = tile_cut(s);
   w.slots = mol_slots(s.nq, s.n_mol, w.cut.rows);
   w.delta = 0;
   w.nlse2 = up256(sizeof(float) * size_t(s.nq) * s.H);
@@ -672,10 +688,31 @@ MolBwdWs bwd_ws(const egat_mol_shape& s) {
   return w;
 }
 
+// q, k and the values by head
+struct MolPackWs {
+  size_t k, v, total;
+};
+MolPackWs pack_ws(const egat_mol_shape& s) {
+  MolPackWs w;
+  w.k = up256(size_t(s.nq) * s.H * s.dk * 2);
+  w.v = w.k + up256(size_t(s.nk) * s.H * s.dk * 2);
+  w.total = w.v + up256(size_t(s.nk) * s.H * head_columns(s) * 2);
+  return w;
+}
+int pack(const egat_mol_shape& s, MolParams& p, void* d_ws, cudaStream_t st) {
+  const MolPackWs w = pack_ws(s);
+  const char* base = static_cast<const char*>(d_ws);
+  p.qp = reinterpret_cast<const uint4*>(base);
+  p.kp = reinterpret_cast<const uint4*>(base + w.k);
+  p.vp = reinterpret_cast<const uint4*>(base + w.v);
+  return mol_umma_pack(p, st);
+}
+
 }  // namespace
 
 size_t molecule_ws_bytes(const egat_mol_shape& s) {
   const MolCut c = forward_cut(s);
+  if (c.umma) return pack_ws(s).total;
   if (c.splits == 1) return 0;
   const size_t rows = size_t(c.splits) * s.nq * s.H;
   return up256(rows * head_columns(s) * sizeof(float)) + up256(rows * 2 * sizeof(float));
@@ -689,6 +726,11 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
   const MolCut c = forward_cut(s);
   p.splits = c.splits;
   p.rwlog = c.rwlog;
+  if (c.umma) {
+    p.slots = mol_slots(s.nq, s.n_mol, c.rows);
+    const int rc = pack(s, p, d_ws, st);
+    return rc != EGAT_OK ? rc : mol_umma_forward(p, c.umma, st);
+  }
   if (p.splits > 1) {
     p.part_o = static_cast<float*>(d_ws);
     p.part_ml = reinterpret_cast<float*>(static_cast<char*>(d_ws) +

@@ -20,6 +20,7 @@ struct MolParams {
   float* part_dq;      // [groups][nq][3] dL/dr of the query atoms, by group of heads
   float* part_dk;      // [groups][nk][3] dL/dr of the key atoms
   float* part_ds;      // [H][slots] dL/dslope, by query tile
+  const uint4 *qp, *kp, *vp;   // q, k and the values by head (molecule_umma.cuh)
   int nq, nk, nmol, D, C, H, dk;
   int ch;              // channels of a head, C / H
   int ch8log;          // log2(ch / 8)
@@ -116,5 +117,10 @@ int mol_tc_heads(const egat_mol_shape& s);   // heads a warp takes together
 int mol_tc_forward(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_q(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_k(const MolParams& p, cudaStream_t st);
+// tcgen05 kernels: whether they take the shape, the packing of the operands, and
+// the forward pass in tiles of 128 * groups rows.
+bool mol_umma_supported(const egat_mol_shape& s);
+int mol_umma_pack(const MolParams& p, cudaStream_t st);
+int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st);
 
 }  // namespace egat
