@@ -293,7 +293,7 @@ __device__ __forceinline__ void tc_cap(f32x2 (&x)[N], f32x2 (&fx)[WANT ? N : 1])
     f2_unpack(x[i], a, b);
     top = tc_max3(top, fabsf(a), fabsf(b));
   }
-  if (top > 1.f) {   // a NaN logit stays NaN either way
+  if (__builtin_expect(top > 1.f, 0)) {   // a NaN logit stays NaN either way
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float a, b, da, db;

@@ -238,9 +238,7 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
       // base-2 scores of the row plus r
       auto scores = [&](float r) {
         uint32_t s[64];
-        um_ld32(ts, s);
-        um_ld32(ts + 32, s + 32);
-        um_ld_done<64>(s);
+        um_ld64(ts, s);
         const f32x2 rr = f2_set(r);
 #pragma unroll
         for (int e = 0; e < 32; ++e) w[e] = f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
@@ -291,15 +289,18 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
           w[e] = f2_pack(2 * e < left ? a : -INFINITY, 2 * e + 1 < left ? b : -INFINITY);
         }
       };
-      bool move = true;
-      if (i > 0) {
-        scores(ref);
+      // once with the reference and, where that has to move, once without: one
+      // copy of the code, which would not fit the instruction cache twice
+      bool move = i == 0;
+#pragma unroll 1
+      for (;;) {
+        scores(move ? 0.f : ref);
         if (left < kUmStage) mask();
-        move = !(row_max() <= 8.f) || isnan(ref);
+        if (move) break;
+        move = __any_sync(~0u, !(row_max() <= 8.f) || isnan(ref));
+        if (!move) break;
       }
-      if (__any_sync(~0u, move)) {
-        scores(0.f);
-        if (left < kUmStage) mask();
+      if (__builtin_expect(move, 0)) {
         const float up = fmaxf(-ref, row_max());   // a NaN reference drops out
         const bool empty = up == -INFINITY;        // all -inf so far
         const float f = empty || isnan(ref) ? 0.f : fast_exp2(-ref - up);
@@ -316,7 +317,6 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
           for (int c = 0; c < L.nt; ++c) {
             uint32_t o[8];
             um_ld8(tm + 2 * kUmStage + c * 8, o);
-            um_ld_done<8>(o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             um_st8(tm + 2 * kUmStage + c * 8, o);
@@ -355,7 +355,6 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
         uint32_t o[8] = {};
         if (stages > 0) {
           um_ld8(tm + 2 * kUmStage + c * 8, o);
-          um_ld_done<8>(o);
         }
         float v[8];
 #pragma unroll

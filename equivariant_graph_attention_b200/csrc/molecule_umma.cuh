@@ -60,27 +60,27 @@ __device__ __forceinline__ void um_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void um_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void um_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void um_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-// Ties registers to the wait for their load: nothing reads them before it.
-template <int N>
-__device__ __forceinline__ void um_ld_done(uint32_t* r) {
-  um_ld_wait();
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
 __device__ __forceinline__ void um_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 #define EGAT_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define EGAT_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-// consecutive 32-bit columns of this thread's lane
-__device__ __forceinline__ void um_ld32(uint32_t t, uint32_t* r) {
+// 64 consecutive 32-bit columns of this thread's lane; the wait is part of it, so
+// that nothing can read them early
+__device__ __forceinline__ void um_ld64(uint32_t t, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      : EGAT_R8(r, 0), EGAT_R8(r, 8), EGAT_R8(r, 16), EGAT_R8(r, 24) : "r"(t));
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : EGAT_R8(r, 0), EGAT_R8(r, 8), EGAT_R8(r, 16), EGAT_R8(r, 24), EGAT_R8(r, 32), EGAT_R8(r, 40), EGAT_R8(r, 48),
+        EGAT_R8(r, 56)
+      : "r"(t) : "memory");
 }
 __device__ __forceinline__ void um_ld8(uint32_t t, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n" : EGAT_R8(r, 0) : "r"(t));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : EGAT_R8(r, 0) : "r"(t) : "memory");
 }
 __device__ __forceinline__ void um_st8(uint32_t t, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::EGAT_I8(r, 0), "r"(t)
