@@ -688,31 +688,11 @@ MolBwdWs bwd_ws(const egat_mol_shape& s) {
   return w;
 }
 
-// q, k and the values by head
-struct MolPackWs {
-  size_t k, v, total;
-};
-MolPackWs pack_ws(const egat_mol_shape& s) {
-  MolPackWs w;
-  w.k = up256(size_t(s.nq) * s.H * s.dk * 2);
-  w.v = w.k + up256(size_t(s.nk) * s.H * s.dk * 2);
-  w.total = w.v + up256(size_t(s.nk) * s.H * head_columns(s) * 2);
-  return w;
-}
-int pack(const egat_mol_shape& s, MolParams& p, void* d_ws, cudaStream_t st) {
-  const MolPackWs w = pack_ws(s);
-  const char* base = static_cast<const char*>(d_ws);
-  p.qp = reinterpret_cast<const uint4*>(base);
-  p.kp = reinterpret_cast<const uint4*>(base + w.k);
-  p.vp = reinterpret_cast<const uint4*>(base + w.v);
-  return mol_umma_pack(p, st);
-}
-
 }  // namespace
 
 size_t molecule_ws_bytes(const egat_mol_shape& s) {
   const MolCut c = forward_cut(s);
-  if (c.umma) return pack_ws(s).total;
+  if (c.umma) return up256(mol_umma_key_bytes(s)) + up256(mol_umma_query_bytes(s, c.umma));
   if (c.splits == 1) return 0;
   const size_t rows = size_t(c.splits) * s.nq * s.H;
   return up256(rows * head_columns(s) * sizeof(float)) + up256(rows * 2 * sizeof(float));
@@ -728,7 +708,10 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
   p.rwlog = c.rwlog;
   if (c.umma) {
     p.slots = mol_slots(s.nq, s.n_mol, c.rows);
-    const int rc = pack(s, p, d_ws, st);
+    p.kv_slots = mol_slots(s.nk, s.n_mol, 64);
+    p.kv = d_ws;
+    p.qp = static_cast<char*>(d_ws) + up256(mol_umma_key_bytes(s));
+    const int rc = mol_umma_pack(p, c.umma, st);
     return rc != EGAT_OK ? rc : mol_umma_forward(p, c.umma, st);
   }
   if (p.splits > 1) {

@@ -20,7 +20,8 @@ struct MolParams {
   float* part_dq;      // [groups][nq][3] dL/dr of the query atoms, by group of heads
   float* part_dk;      // [groups][nk][3] dL/dr of the key atoms
   float* part_ds;      // [H][slots] dL/dslope, by query tile
-  const uint4 *qp, *kp, *vp;   // q, k and the values by head (molecule_umma.cuh)
+  void *qp, *kv;       // operand blocks of the tcgen05 kernels
+  int kv_slots;        // key blocks of a head
   int nq, nk, nmol, D, C, H, dk;
   int ch;              // channels of a head, C / H
   int ch8log;          // log2(ch / 8)
@@ -60,6 +61,7 @@ __device__ __forceinline__ int mol_start(const int32_t* ptr, int nmol, int n, in
 struct MolTile {
   int row0, rows;    // own rows; rows <= 0: nothing to do
   int o0, o1;        // rows of the other side it meets
+  int seg;           // its segment
 };
 // The tile of a slot (M = 2^mlog); called by whole warps (32-way bisection).
 __device__ __forceinline__ MolTile mol_tile(int mlog, const int32_t* ptr, const int32_t* optr, int nmol,
@@ -82,6 +84,7 @@ __device__ __forceinline__ MolTile mol_tile(int mlog, const int32_t* ptr, const 
   const bool some = e > s && off <= ((e - s) >> mlog);
   t.row0 = some ? s + (off << mlog) : 0;
   t.rows = some ? min(M, e - t.row0) : 0;
+  t.seg = lo;
   const bool mol = lo > 0 && lo <= nmol;
   t.o0 = mol ? mol_start(optr, nmol, on, lo) : 0;
   t.o1 = mol ? max(t.o0, mol_start(optr, nmol, on, lo + 1)) : 0;
@@ -117,10 +120,12 @@ int mol_tc_heads(const egat_mol_shape& s);   // heads a warp takes together
 int mol_tc_forward(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_q(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_k(const MolParams& p, cudaStream_t st);
-// tcgen05 kernels: whether they take the shape, the packing of the operands, and
-// the forward pass in tiles of 128 * groups rows.
+// tcgen05 kernels: whether they take the shape, the sizes of the operand blocks
+// and their packing, and the forward pass in tiles of 128 * groups rows.
 bool mol_umma_supported(const egat_mol_shape& s);
-int mol_umma_pack(const MolParams& p, cudaStream_t st);
+size_t mol_umma_key_bytes(const egat_mol_shape& s);
+size_t mol_umma_query_bytes(const egat_mol_shape& s, int groups);
+int mol_umma_pack(const MolParams& p, int groups, cudaStream_t st);
 int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st);
 
 }  // namespace egat

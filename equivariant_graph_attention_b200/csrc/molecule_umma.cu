@@ -1,79 +1,120 @@
 // Attention within each molecule on the fifth-generation tensor cores: the
 // forward pass over long molecules (bf16 storage).
 //
-// A CTA takes one head and 128 G query rows of a molecule, in G groups of four
-// warps whose lanes are rows, and passes over the keys in stages of 64:
+// A CTA takes one head and 128 G query rows of a molecule, in G groups of eight
+// warps, and passes over the keys in stages of 64:
 //  * one warp brings the stages in (bulk copies, one per chunk, three stages in
 //    flight) and writes their positions;
 //  * one thread issues the products: S = Q K^T into one of a group's two
 //    64-column score buffers in tensor memory, and m += P H' with P from tensor
 //    memory, where it replaces the scores;
-//  * a thread of a group reads the 64 scores of its row, applies cap, bias and
-//    exponential, and writes its weights back as bf16.  A row is one thread's:
-//    maximum and normaliser need no exchange.  The row's reference moves only when
-//    a score passes it by 2^8; then the accumulator is rescaled in place.
+//  * a row of a group is two threads', of two warps that share its lanes: each
+//    reads 32 of its 64 scores, applies cap, bias and exponential, and writes its
+//    weights back as bf16.  (One thread with all 64 left two warps a scheduler,
+//    which waited most of the time: 0.71 ms at 8,191 atoms and lmax 3.)  The row's
+//    reference moves only when a score passes it by 2^8; only then do the two
+//    exchange their maxima, and the accumulator is rescaled in place.
 // While a group works on one stage, the tensor core forms its next scores and
 // the other group's products.  Work per pair and head is one exponential (and one
 // root with a bias) on the special-function unit, which is what bounds it: the
 // products take a quarter of that at 16 + 72 columns.  Every wait is bounded.
+#include <algorithm>
+
 #include "molecule_umma.cuh"
 
 namespace egat {
 namespace {
 
-// [n][row] bf16 tensors into [head][chunk][n] chunks of 8 columns, 64 rows and up
-// to 16 chunks a block through shared memory, read and written in whole runs.
-struct PackJob {
-  const uint4* src;
-  uint4* dst;
-  int n, row_chunks;   // rows, chunks of a row
-  int head_chunks;     // chunks of a head in a run of heads (its channels / 8, or dk / 8)
-  int run_chunks;      // chunks of one run of heads (C / 8, or a whole row)
-  int dst_chunks;      // chunks of a head in dst
-  int slices;          // blocks over a row: 16 chunks each
-  int blocks;          // 64-row blocks
+// Operand blocks of a shape, in bytes; one of them is one bulk copy.
+struct UmBlocks {
+  int nt, nv;        // value chunks, and to a multiple of 16 columns (the last chunk zeros)
+  int ks;            // k-steps of 16 of a score
+  int v, pos, key;   // key block: [2 ks chunks][64][16 B], values [nv][64][16 B], x[64], y[64], z[64]
+  int query;         // query block of a group: [2 ks chunks][128][16 B]
+  __host__ __device__ UmBlocks(int dv, int dk) {
+    nt = dv >> 3;
+    nv = (nt + 1) & ~1;
+    ks = dk > 16 ? 2 : 1;
+    v = 2 * ks * kUmStage * 16;
+    pos = v + nv * kUmStage * 16;
+    key = pos + kUmStage * 16;
+    query = 2 * ks * kUmRows * 16;
+  }
 };
-struct PackArgs {
-  PackJob job[3];
-};
-__global__ void __launch_bounds__(256) mol_pack_kernel(PackArgs args) {
+
+// q, k, the values and the key positions into those blocks, by head and tile (64
+// keys; groups * 128 query rows): 64 rows and up to 16 chunks a block through shared
+// memory, read and written in whole runs.  Rows past a tile are zeros.
+__global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slots, int query_slots, int mlog) {
+  const UmBlocks B(p.dv, p.dk);
   __shared__ uint4 sm[64][17];
-  int b = blockIdx.x, which = 0;
-  while (b >= args.job[which].slices * args.job[which].blocks) b -= args.job[which].slices * args.job[which++].blocks;
-  const PackJob& j = args.job[which];
-  const int row0 = (b / j.slices) * 64, c0 = (b % j.slices) * 16;
+  const bool keys = int(blockIdx.x) < key_slots;
+  const int slot = keys ? blockIdx.x : blockIdx.x - key_slots;
+  const MolTile t = keys ? mol_tile(6, p.a.kptr, p.a.kptr, p.nmol, p.nk, p.nk, slot)
+                         : mol_tile(mlog, p.a.qptr, p.a.qptr, p.nmol, p.nq, p.nq, slot);
+  if (t.rows <= 0) return;
+  const int qk_chunks = p.H * p.dk / 8, qk_slices = (qk_chunks + 15) / 16;
+  const int val_chunks = p.D * p.C / 8, val_slices = (val_chunks + 15) / 16;
+  int y = blockIdx.y, sub = 0;
+  if (!keys) {   // 64 rows of the tile, slices of q
+    const int subs = 1 << (mlog - 6);
+    sub = y % subs;
+    y /= subs;
+  }
+  const int last = keys ? qk_slices + val_slices : qk_slices;
+  if (y > last) return;
+  const int row0 = t.row0 + sub * 64, rows = min(64, t.rows - sub * 64);   // may be below one: zeros
+  const int kc = p.dk >> 3, vc = p.ch >> 3, run = p.C >> 3;
+  unsigned char* const out = static_cast<unsigned char*>(keys ? p.kv : p.qp);
+  const size_t block = keys ? B.key : size_t(B.query) << (mlog - 7), slots = keys ? key_slots : query_slots;
+  const size_t in_block = keys ? 0 : size_t(sub >> 1) * B.query + (sub & 1) * 64 * 16;
+  const int chunk_bytes = keys ? kUmStage * 16 : kUmRows * 16;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (y == last) {   // what no tensor fills, and positions
+    for (int h = 0; h < p.H; ++h) {
+      unsigned char* o = out + (h * slots + slot) * block + in_block;
+      for (int r = threadIdx.x; r < 64; r += blockDim.x) {
+        if (kc == 1) *reinterpret_cast<uint4*>(o + chunk_bytes + r * 16) = zero;
+        if (keys && B.nv > B.nt) *reinterpret_cast<uint4*>(o + B.v + B.nt * chunk_bytes + r * 16) = zero;
+        if (keys && p.a.slope)
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            *reinterpret_cast<float*>(o + B.pos + (c * kUmStage + r) * 4) =
+                r < rows ? p.a.posk[size_t(row0 + r) * 3 + c] : 0.f;
+      }
+    }
+    return;
+  }
+  const bool val = y >= qk_slices;
+  const int c0 = (val ? y - qk_slices : y) * 16, chunks = val ? val_chunks : qk_chunks;
+  const uint4* src = static_cast<const uint4*>(val ? p.a.hp : keys ? p.a.k : p.a.q);
   const int c = threadIdx.x & 15;
   for (int r = threadIdx.x >> 4; r < 64; r += 16)
-    if (row0 + r < j.n && c0 + c < j.row_chunks) sm[r][c] = __ldg(j.src + size_t(row0 + r) * j.row_chunks + c0 + c);
+    if (c0 + c < chunks) sm[r][c] = r < rows ? __ldg(src + size_t(row0 + r) * chunks + c0 + c) : zero;
   __syncthreads();
   const int r = threadIdx.x & 63;
-  for (int i = threadIdx.x >> 6; i < 16; i += 4)
-    if (row0 + r < j.n && c0 + i < j.row_chunks) {
-      const int x = c0 + i, run = x / j.run_chunks, in = x - run * j.run_chunks;
-      const int head = in / j.head_chunks, chunk = run * j.head_chunks + in - head * j.head_chunks;
-      j.dst[(size_t(head) * j.dst_chunks + chunk) * j.n + row0 + r] = sm[r][i];
-    }
+  for (int i = threadIdx.x >> 6; i < 16; i += 4) {
+    const int x = c0 + i;
+    if (x >= chunks) break;
+    const int d = val ? x / run : 0, in = val ? x - d * run : x, per = val ? vc : kc, head = in / per;
+    const int chunk = d * per + in - head * per;
+    *reinterpret_cast<uint4*>(out + (head * slots + slot) * block + in_block + (val ? B.v : 0) + chunk * chunk_bytes +
+                              r * 16) = sm[r][i];
+  }
 }
 
 constexpr int kUmStages = 3;
 
-// Shared memory of a CTA, in bytes; the numbers of chunks are those of the shape.
+// Shared memory of a CTA
 template <int G>
-struct UmLay {
+struct UmLay : UmBlocks {
   static constexpr int NBARS = 2 * kUmStages + 1 + 6 * G;
   static constexpr int COLS = 256 * G;   // per group: scores 2 x 64, accumulator up to 128
-  int nt, nv;      // value chunks, and to a multiple of 16 columns (the last chunk zeros)
-  int ks;          // k-steps of 16 of a score
-  int v, pos, stage, q, bars, slot, flag, total;
-  __host__ __device__ UmLay(int dv, int dk) {
-    nt = dv >> 3;
-    nv = (nt + 1) & ~1;
-    ks = dk > 16 ? 2 : 1;
-    v = 2 * ks * kUmStage * 16;               // after keys [2 ks chunks][64][16 B]: values [nv][64][16 B]
-    pos = v + nv * kUmStage * 16;             // x[64], y[64], z[64]
-    stage = pos + kUmStage * 16;
-    q = kUmStages * stage;                    // [G][2 ks chunks][128][16 B]
-    bars = q + G * 2 * ks * kUmRows * 16;
+  int q, pair, bars, slot, flag, total;  // after the stages
+  __host__ __device__ UmLay(int dv, int dk) : UmBlocks(dv, dk) {
+    q = kUmStages * key;
+    pair = q + G * query;                  // [4 G pairs of warps][2][32] maxima or sums, then [..][2][2] flags
+    bars = pair + 4 * G * (64 + 4) * 4;
     slot = bars + 8 * NBARS;
     flag = slot + 4;
     total = flag + 12;
@@ -81,7 +122,7 @@ struct UmLay {
 };
 
 template <int G, bool CAP, bool BIAS>
-__global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma_kernel(MolParams p) {
+__global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma_kernel(MolParams p) {
   const UmLay<G> L(p.dv, p.dk);
   extern __shared__ __align__(128) unsigned char um[];
   const int head = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -101,8 +142,6 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
   const int n = t.o1 - t.o0, stages = (n + kUmStage - 1) / kUmStage;
   const int groups = (t.rows + kUmRows - 1) / kUmRows;   // groups with rows
 
-  // rows that no copy fills are zeros, not what was there before
-  for (int i = threadIdx.x; i < L.bars / 16; i += blockDim.x) reinterpret_cast<uint4*>(um)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kUmStages; ++s) {
       mbar_init(full(s), 1);
@@ -112,53 +151,36 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
     for (int g = 0; g < G; ++g) {
       mbar_init(sfull(g, 0), 1);
       mbar_init(sfull(g, 1), 1);
-      mbar_init(pready(g, 0), 4);
-      mbar_init(pready(g, 1), 4);
+      mbar_init(pready(g, 0), 8);
+      mbar_init(pready(g, 1), 8);
       mbar_init(pvdone(g, 0), 1);
       mbar_init(pvdone(g, 1), 1);
     }
     mbar_fence_init();
     *abort_flag = 0;
   }
-  if (warp == 4 * G) um_alloc<UmLay<G>::COLS>(base + L.slot);
-  fence_proxy_async_smem();
+  if (warp == 8 * G) um_alloc<UmLay<G>::COLS>(base + L.slot);
   um_before();
   __syncthreads();
   um_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(um + L.slot);
 
-  if (warp == 4 * G + 1) {
+  if (warp == 8 * G + 1) {
     // ---- stages
-    const int kc = p.dk >> 3;
+    const unsigned char* kv = static_cast<const unsigned char*>(p.kv) +
+                              (size_t(head) * p.kv_slots + (t.o0 >> 6) + t.seg) * L.key;
     if (lane == 0 && stages > 0) {
-      mbar_arrive_expect_tx(qfull, uint32_t(t.rows * kc * 16));
-      for (int g = 0; g < groups; ++g) {
-        const int rows = min(kUmRows, t.rows - g * kUmRows);
-        for (int c = 0; c < kc; ++c)
-          bulk_g2s(base + L.q + (g * 2 * L.ks + c) * kUmRows * 16,
-                   p.qp + (size_t(head) * kc + c) * p.nq + t.row0 + g * kUmRows, rows * 16, qfull);
+      mbar_arrive_expect_tx(qfull, G * L.query);
+      bulk_g2s(base + L.q, static_cast<const unsigned char*>(p.qp) + (size_t(head) * p.slots + blockIdx.x) * G * L.query,
+               G * L.query, qfull);
+      for (int i = 0; i < stages; ++i) {
+        const int s = i % kUmStages;
+        if (i >= kUmStages && !bounded_wait(freed(s), (i / kUmStages - 1) & 1, kWaitPolls, abort_flag)) break;
+        mbar_arrive_expect_tx(full(s), L.key);
+        bulk_g2s(base + s * L.key, kv + size_t(i) * L.key, L.key, full(s));
       }
     }
-    for (int i = 0; i < stages; ++i) {
-      const int s = i % kUmStages, k0 = t.o0 + i * kUmStage, rows = min(kUmStage, t.o1 - k0);
-      if (i >= kUmStages && !bounded_wait(freed(s), (i / kUmStages - 1) & 1, kWaitPolls, abort_flag)) break;
-      if (BIAS) {
-        float* sp = reinterpret_cast<float*>(um + s * L.stage + L.pos);
-        for (int r = lane; r < rows; r += 32)
-#pragma unroll
-          for (int c = 0; c < 3; ++c) sp[c * kUmStage + r] = __ldg(p.a.posk + size_t(k0 + r) * 3 + c);
-      }
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t st = base + s * L.stage;
-        mbar_arrive_expect_tx(full(s), uint32_t((kc + L.nt) * rows * 16));
-        for (int c = 0; c < kc; ++c)
-          bulk_g2s(st + c * kUmStage * 16, p.kp + (size_t(head) * kc + c) * p.nk + k0, rows * 16, full(s));
-        for (int c = 0; c < L.nt; ++c)
-          bulk_g2s(st + L.v + c * kUmStage * 16, p.vp + (size_t(head) * L.nt + c) * p.nk + k0, rows * 16, full(s));
-      }
-      __syncwarp();
-    }
+    __syncwarp();
     if (*abort_flag && lane == 0) {   // copies in flight land before the memory is given up
       volatile int none = 0;
       if (stages > 0) bounded_wait(qfull, 0, kDrainPolls, &none);
@@ -168,12 +190,12 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
         if (last >= 0) bounded_wait(full(s), (last / kUmStages) & 1, kDrainPolls, &none);
       }
     }
-  } else if (warp == 4 * G) {
+  } else if (warp == 8 * G) {
     // ---- products
     if (lane == 0 && stages > 0) {
       bool ok = bounded_wait(qfull, 0, kWaitPolls, abort_flag);
       auto scores = [&](int i, int g) {
-        const uint32_t st = base + (i % kUmStages) * L.stage;
+        const uint32_t st = base + (i % kUmStages) * L.key;
 #pragma unroll
         for (int k = 0; k < L.ks; ++k)
           um_mma_ss(tmem + g * 256 + (i & 1) * kUmStage,
@@ -196,7 +218,7 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
           ok = bounded_wait(pready(g, i & 1), (i >> 1) & 1, kWaitPolls, abort_flag);
           if (!ok) break;
           um_after();
-          const uint32_t st = base + (i % kUmStages) * L.stage;
+          const uint32_t st = base + (i % kUmStages) * L.key;
 #pragma unroll
           for (int k = 0; k < kUmStage / 16; ++k)
             um_mma_ts(tmem + g * 256 + 2 * kUmStage, tmem + g * 256 + (i & 1) * kUmStage + k * 8,
@@ -207,12 +229,16 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
       }
     }
     __syncwarp();
-  } else if ((warp >> 2) < groups) {
-    // ---- softmax: a thread is a row
-    const int g = warp >> 2, own = g * kUmRows + (warp & 3) * 32 + lane;
+  } else if ((warp >> 3) < groups) {
+    // ---- softmax: a row is two threads'
+    const int g = warp >> 3, half = (warp >> 2) & 1, own = g * kUmRows + (warp & 3) * 32 + lane;
     const bool live = own < t.rows;
     const size_t row = size_t(t.row0) + (live ? own : 0);
     const uint32_t tm = tmem + (uint32_t((warp & 3) * 32) << 16) + g * 256;
+    const int pair = g * 4 + (warp & 3);
+    volatile float* shared_row = reinterpret_cast<float*>(um + L.pair) + pair * 64 + lane;   // [half] * 32
+    volatile int* flags = reinterpret_cast<int*>(um + L.pair) + 4 * G * 64 + pair * 4;         // [stage & 1][half]
+    auto sync_pair = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(1 + pair) : "memory"); };
     f32x2 px = 0, py = 0, pz = 0, slope = 0;
     if (BIAS) {
       const float* x = p.a.posq + row * 3;
@@ -225,26 +251,30 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
     const float none = __int_as_float(0x7fffffff);
     float ref = none;   // minus the reference; NaN: none yet
     f32x2 sum = 0;
+    // a wait that gave up does not end the loop: the pair's barriers need both warps,
+    // and later waits return at once
     bool ok = true;
     for (int i = 0; i < stages; ++i) {
-      ok = um_wait(sfull(g, i & 1), (i >> 1) & 1, abort_flag);
-      if (BIAS) ok = ok && um_wait(full(i % kUmStages), (i / kUmStages) & 1, abort_flag);   // its positions
-      if (!ok) break;
+      ok = um_wait(sfull(g, i & 1), (i >> 1) & 1, abort_flag) && ok;
+      if (BIAS) ok = um_wait(full(i % kUmStages), (i / kUmStages) & 1, abort_flag) && ok;   // its positions
       um_after();
       const uint32_t ts = tm + (i & 1) * kUmStage;
-      const int left = n - i * kUmStage;
-      const float* sp = reinterpret_cast<const float*>(um + (i % kUmStages) * L.stage + L.pos);
-      f32x2 w[32];
-      // base-2 scores of the row plus r
-      auto scores = [&](float r) {
-        uint32_t s[64];
-        um_ld64(ts, s);
-        const f32x2 rr = f2_set(r);
+      const int left = n - i * kUmStage - half * 32;
+      const float* sp = reinterpret_cast<const float*>(um + (i % kUmStages) * L.key + L.pos) + half * 32;
+      f32x2 w[16];
+      // once with the reference and, where that has to move, once without: one
+      // copy of the code, which would not fit the instruction cache twice
+      bool move = i == 0;
+#pragma unroll 1
+      for (;;) {
+        uint32_t s[32];
+        um_ld32(ts + half * 32, s);
+        const f32x2 rr = f2_set(move ? 0.f : ref);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        for (int e = 0; e < 16; ++e) w[e] = f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
         if constexpr (CAP) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             f32x2 x[8], unused[1];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = f2_mul(w[8 * k + e], c_in);
@@ -254,10 +284,10 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
           }
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = f2_fma(w[e], CAP ? c_cap : c_in, rr);
+        for (int e = 0; e < 16; ++e) w[e] = f2_fma(w[e], CAP ? c_cap : c_in, rr);
         if constexpr (BIAS) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sp + 2 * e);
             const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sp + kUmStage + 2 * e);
             const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(sp + 2 * kUmStage + 2 * e);
@@ -270,51 +300,45 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
             }
           }
         }
-      };
-      auto row_max = [&]() {
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (left < 32) {   // keys past the molecule
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            f2_unpack(w[e], a, b);
+            w[e] = f2_pack(2 * e < left ? a : -INFINITY, 2 * e + 1 < left ? b : -INFINITY);
+          }
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
           float a, b;
           f2_unpack(w[e], a, b);
-          m[e & 3] = tc_max3(m[e & 3], a, b);
+          top[e & 1] = tc_max3(top[e & 1], a, b);
         }
-        return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-      };
-      auto mask = [&]() {   // keys past the molecule
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float a, b;
-          f2_unpack(w[e], a, b);
-          w[e] = f2_pack(2 * e < left ? a : -INFINITY, 2 * e + 1 < left ? b : -INFINITY);
+        const float mx = fmaxf(top[0], top[1]);
+        if (!move) {
+          move = __any_sync(~0u, !(mx <= 8.f) || isnan(ref));
+          if (lane == 0) flags[(i & 1) * 2 + half] = move;
+          sync_pair();   // both have read their scores, too: the weights may replace them
+          move = flags[(i & 1) * 2] | flags[(i & 1) * 2 + 1];
+          if (!move) break;
+          continue;
         }
-      };
-      // once with the reference and, where that has to move, once without: one
-      // copy of the code, which would not fit the instruction cache twice
-      bool move = i == 0;
-#pragma unroll 1
-      for (;;) {
-        scores(move ? 0.f : ref);
-        if (left < kUmStage) mask();
-        if (move) break;
-        move = __any_sync(~0u, !(row_max() <= 8.f) || isnan(ref));
-        if (!move) break;
-      }
-      if (__builtin_expect(move, 0)) {
-        const float up = fmaxf(-ref, row_max());   // a NaN reference drops out
-        const bool empty = up == -INFINITY;        // all -inf so far
+        shared_row[half * 32] = mx;
+        sync_pair();
+        const float up = fmaxf(-ref, fmaxf(shared_row[0], shared_row[32]));   // a NaN reference drops out
+        const bool empty = up == -INFINITY;                                    // all -inf so far
         const float f = empty || isnan(ref) ? 0.f : fast_exp2(-ref - up);
         ref = empty ? none : -up;
         sum = f2_mul(sum, f2_set(f));
         const f32x2 shift = f2_set(empty ? 0.f : -up);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = f2_add(w[e], shift);
+        for (int e = 0; e < 16; ++e) w[e] = f2_add(w[e], shift);
         if (i > 0) {   // rescale the accumulator, once the last stage's product is in it
-          ok = um_wait(pvdone(g, (i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag);
-          if (!ok) break;
+          ok = um_wait(pvdone(g, (i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag) && ok;
           um_after();
 #pragma unroll 1
-          for (int c = 0; c < L.nt; ++c) {
+          for (int c = half; c < L.nt; c += 2) {
             uint32_t o[8];
             um_ld8(tm + 2 * kUmStage + c * 8, o);
 #pragma unroll
@@ -323,20 +347,21 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
           }
           um_st_wait();
         }
+        break;
       }
-      uint32_t pk[32];
-      f32x2 part[4] = {0, 0, 0, 0};
+      uint32_t pk[16];
+      f32x2 part[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < 16; ++e) {
         float a, b;
         f2_unpack(w[e], a, b);
         a = fast_exp2(a);
         b = fast_exp2(b);
-        part[e & 3] = f2_add(part[e & 3], f2_pack(a, b));
+        part[e & 1] = f2_add(part[e & 1], f2_pack(a, b));
         pk[e] = tc_pack(a, b);
       }
-      sum = f2_add(sum, f2_add(f2_add(part[0], part[1]), f2_add(part[2], part[3])));
-      um_st32(ts, pk);
+      sum = f2_add(sum, f2_add(part[0], part[1]));
+      um_st16(ts + half * 16, pk);
       um_st_wait();
       um_before();
       __syncwarp();
@@ -346,16 +371,17 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
     um_after();
     float l0, l1;
     f2_unpack(sum, l0, l1);
-    const float l = l0 + l1, inv = l == 0.f ? 0.f : 1.f / l;
-    if (live && p.lse) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : -ref * kLn2 + logf(l);
+    sync_pair();   // the maxima have been read
+    shared_row[half * 32] = l0 + l1;
+    sync_pair();
+    const float l = shared_row[0] + shared_row[32], inv = l == 0.f ? 0.f : 1.f / l;
+    if (live && half == 0 && p.lse) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : -ref * kLn2 + logf(l);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.m) + row * (p.D * p.C);
     if (ok)
 #pragma unroll 1
-      for (int c = 0; c < L.nt; ++c) {
+      for (int c = half; c < L.nt; c += 2) {
         uint32_t o[8] = {};
-        if (stages > 0) {
-          um_ld8(tm + 2 * kUmStage + c * 8, o);
-        }
+        if (stages > 0) um_ld8(tm + 2 * kUmStage + c * 8, o);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
@@ -364,43 +390,33 @@ __global__ void __launch_bounds__((4 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
               make_uint4(tc_pack(v[0], v[1]), tc_pack(v[2], v[3]), tc_pack(v[4], v[5]), tc_pack(v[6], v[7]));
       }
   }
-  if (*abort_flag && warp == 4 * G && lane == 0) {   // products in flight end before tensor memory is freed
+  if (*abort_flag && warp == 8 * G && lane == 0) {   // products in flight end before tensor memory is freed
     volatile int none = 0;
     um_commit(qfull);   // its second phase: everything issued so far
     bounded_wait(qfull, 1, kDrainPolls, &none);
   }
   um_before();
   __syncthreads();
-  if (warp == 4 * G) {
+  if (warp == 8 * G) {
     um_after();
     um_dealloc<UmLay<G>::COLS>(tmem);
   }
 }
 
-PackJob pack_job(const void* src, void* dst, int n, int row, int head, int run, int heads) {
-  PackJob j;
-  j.src = static_cast<const uint4*>(src);
-  j.dst = static_cast<uint4*>(dst);
-  j.n = n;
-  j.row_chunks = row / 8;
-  j.head_chunks = head / 8;
-  j.run_chunks = run / 8;
-  j.dst_chunks = j.row_chunks / heads;
-  j.slices = (j.row_chunks + 15) / 16;
-  j.blocks = (n + 63) / 64;
-  return j;
-}
-
 }  // namespace
 
-int mol_umma_pack(const MolParams& p, cudaStream_t st) {
-  PackArgs a;
-  a.job[0] = pack_job(p.a.q, const_cast<uint4*>(p.qp), p.nq, p.H * p.dk, p.dk, p.H * p.dk, p.H);
-  a.job[1] = pack_job(p.a.k, const_cast<uint4*>(p.kp), p.nk, p.H * p.dk, p.dk, p.H * p.dk, p.H);
-  a.job[2] = pack_job(p.a.hp, const_cast<uint4*>(p.vp), p.nk, p.D * p.C, p.ch, p.C, p.H);
-  long long blocks = 0;
-  for (const PackJob& j : a.job) blocks += (long long)j.slices * j.blocks;
-  if (blocks > 0) mol_pack_kernel<<<unsigned(blocks), 256, 0, st>>>(a);
+size_t mol_umma_key_bytes(const egat_mol_shape& s) {
+  return size_t(mol_slots(s.nk, s.n_mol, kUmStage)) * s.H *
+         UmBlocks((s.lmax + 1) * (s.lmax + 1) * (s.C / s.H), s.dk).key;
+}
+size_t mol_umma_query_bytes(const egat_mol_shape& s, int groups) {
+  return size_t(mol_slots(s.nq, s.n_mol, kUmRows * groups)) * s.H * groups * UmBlocks(8, s.dk).query;
+}
+
+int mol_umma_pack(const MolParams& p, int groups, cudaStream_t st) {
+  const int qk = (p.H * p.dk / 8 + 15) / 16, val = (p.D * p.C / 8 + 15) / 16, subs = 2 * groups;
+  const dim3 grid(p.kv_slots + p.slots, std::max(qk + val + 1, (qk + 1) * subs));
+  mol_pack_kernel<<<grid, 256, 0, st>>>(p, p.kv_slots, p.slots, groups == 2 ? 8 : 7);
   return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA;
 }
 
@@ -414,8 +430,8 @@ int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st) {
   return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
     constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
     const dim3 grid(p.slots, p.H);
-    return groups == 2 ? mol_launch(mol_fwd_umma_kernel<2, CAP, BIAS>, grid, 320, UmLay<2>(p.dv, p.dk).total, p, st)
-                       : mol_launch(mol_fwd_umma_kernel<1, CAP, BIAS>, grid, 192, UmLay<1>(p.dv, p.dk).total, p, st);
+    return groups == 2 ? mol_launch(mol_fwd_umma_kernel<2, CAP, BIAS>, grid, 576, UmLay<2>(p.dv, p.dk).total, p, st)
+                       : mol_launch(mol_fwd_umma_kernel<1, CAP, BIAS>, grid, 320, UmLay<1>(p.dv, p.dk).total, p, st);
   });
 }
 

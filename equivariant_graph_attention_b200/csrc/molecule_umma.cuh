@@ -6,10 +6,10 @@
 // contraction's outer index that is the canonical K-major layout without
 // swizzle, and with rows as the contraction index the canonical MN-major one,
 // so one staged copy of a tensor serves both kinds of product.  A packing kernel
-// lays q, k and the values out in that order for every head ([head][chunk][row]),
-// once a call: a chunk of a tile is then one contiguous bulk copy, and every
-// 32-byte sector that is read is used whole (a head's chunks alone are half a
-// sector of an atom's row).
+// lays the operands out as whole stages by head and tile, once a call: a stage is
+// then one contiguous bulk copy (one copy per chunk, 18 at lmax 3, took the issuing
+// thread 2,500 cycles a stage, twice the exponentials), and every 32-byte sector
+// is used whole, where a head's chunk alone is half a sector of an atom's row.
 #pragma once
 
 #include "egat_async.cuh"
@@ -63,17 +63,14 @@ __device__ __forceinline__ void um_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void um_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 #define EGAT_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define EGAT_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-// 64 consecutive 32-bit columns of this thread's lane; the wait is part of it, so
-// that nothing can read them early
-__device__ __forceinline__ void um_ld64(uint32_t t, uint32_t* r) {
+// Consecutive 32-bit columns of this thread's lane; the wait is part of the load,
+// so that nothing can read them early.
+__device__ __forceinline__ void um_ld32(uint32_t t, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : EGAT_R8(r, 0), EGAT_R8(r, 8), EGAT_R8(r, 16), EGAT_R8(r, 24), EGAT_R8(r, 32), EGAT_R8(r, 40), EGAT_R8(r, 48),
-        EGAT_R8(r, 56)
+      : EGAT_R8(r, 0), EGAT_R8(r, 8), EGAT_R8(r, 16), EGAT_R8(r, 24)
       : "r"(t) : "memory");
 }
 __device__ __forceinline__ void um_ld8(uint32_t t, uint32_t* r) {
@@ -86,11 +83,10 @@ __device__ __forceinline__ void um_st8(uint32_t t, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::EGAT_I8(r, 0), "r"(t)
                : "memory");
 }
-__device__ __forceinline__ void um_st32(uint32_t t, const uint32_t* r) {
+__device__ __forceinline__ void um_st16(uint32_t t, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};\n" ::EGAT_I8(r, 0),
-      EGAT_I8(r, 8), EGAT_I8(r, 16), EGAT_I8(r, 24), "r"(t)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};\n" ::EGAT_I8(r, 0), EGAT_I8(r, 8), "r"(t)
       : "memory");
 }
 #undef EGAT_R8

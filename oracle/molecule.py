@@ -36,7 +36,7 @@ def _unheads(x, D, C):
 
 def _scores(q, k, cap, pos_q, pos_k, slope):
     dk = q.shape[2]
-    x = np.einsum("ihd,jhd->hij", q, k) / np.sqrt(dk)
+    x = q.transpose(1, 0, 2) @ k.transpose(1, 2, 0) / np.sqrt(dk)
     s = cap * np.tanh(x / cap) if cap else x
     if slope is None:
         return x, s, None, None
@@ -71,7 +71,7 @@ def molecule_attention(q, k, hp, q_ptr, k_ptr=None, cap=0.0, pos_q=None, pos_k=N
             continue
         args = (pos_q[i], pos_k[j], slope) if slope is not None else (None, None, None)
         x, s, d, diff = _scores(q[i], k[j], cap, *args)
-        o["score"] = max(o["score"], np.einsum("ihd,jhd->hij", np.abs(q[i]), np.abs(k[j])).max() / np.sqrt(dk))
+        o["score"] = max(o["score"], (np.abs(q[i]).transpose(1, 0, 2) @ np.abs(k[j]).transpose(1, 2, 0)).max() / np.sqrt(dk))
         if d is not None:
             o["dist"] = max(o["dist"], np.abs(slope).max() * d.max())
         top = s.max(2, keepdims=True)
@@ -94,8 +94,8 @@ def molecule_attention(q, k, hp, q_ptr, k_ptr=None, cap=0.0, pos_q=None, pos_k=N
         # 1 - tanh^2 = 1 / cosh^2, without the cancellation
         fx = (np.cosh(x / cap) ** -2 if cap else 1.0) / np.sqrt(dk)
         for p, S, qq, kk in (("", dS * fx, q, k), ("abs_", aS * fx, np.abs(q), np.abs(k))):
-            o[p + "dq"][i] = np.einsum("hij,jhd->ihd", S, kk[j])
-            o[p + "dk"][j] = np.einsum("hij,ihd->jhd", S, qq[i])
+            o[p + "dq"][i] = (S @ kk[j].transpose(1, 0, 2)).transpose(1, 0, 2)
+            o[p + "dk"][j] = (S.transpose(0, 2, 1) @ qq[i].transpose(1, 0, 2)).transpose(1, 0, 2)
         if slope is None:
             continue
         u = np.divide(diff, d[..., None], out=np.zeros_like(diff), where=d[..., None] > 0)
