@@ -25,9 +25,8 @@ constexpr int kMolBatch = 4;   // keys taken together by the online softmax
 
 template <int NV, int LP>
 struct MolRows {
-  static constexpr int KV = LP >= 8 ? 1 : 8 / LP;    // query vectors of a lane (dk <= 32)
-  static constexpr int M = kMolWarps * (32 / LP);    // rows of a tile
-  static constexpr int MLOG = LP == 1 ? 7 : LP == 2 ? 6 : LP == 4 ? 5 : LP == 8 ? 4 : LP == 16 ? 3 : 2;
+  static constexpr int WLOG = LP == 1 ? 5 : LP == 2 ? 4 : LP == 4 ? 3 : LP == 8 ? 2 : LP == 16 ? 1 : 0;
+  static constexpr int W = 1 << WLOG;                // rows of a warp (of one row a lane group)
   static constexpr int DV = 4 * NV * LP;             // value columns
 };
 
@@ -78,9 +77,9 @@ template <int DV, typename T>
 __device__ __forceinline__ void stage_rows(const MolParams& p, int head, const T* qk, const T* val,
                                            const float* pos, int r0, int end, float* sk, float* sv,
                                            float* sp) {
-  const int kv = p.dk / 4;
-  for (int i = threadIdx.x; i < p.kb * kv; i += kMolThreads) {
-    const int r = i / kv, x = i - r * kv;
+  const int kvlog = p.dk == 8 ? 1 : p.dk == 16 ? 2 : 3;   // vectors of a query or key
+  for (int i = threadIdx.x; i < p.kb << kvlog; i += kMolThreads) {
+    const int r = i >> kvlog, x = i & ((1 << kvlog) - 1);
     const bool in = r0 + r < end;
     const float4 v = in ? load4(qk + (size_t(r0 + r) * p.H + head) * p.dk + 4 * x)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -107,24 +106,25 @@ __device__ __forceinline__ void stage_rows(const MolParams& p, int head, const T
 
 // ---- forward
 
-template <int NV, int LP, typename T>
+template <int NV, int LP, int KV, typename T>
 __global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
-  using R = MolRows<NV, LP>;
+  using G = MolRows<NV, LP>;
   extern __shared__ __align__(16) float msm[];
   float* sk = msm;
   float* sv = sk + p.kb * p.dk;
-  float* sp = sv + p.kb * R::DV;
-  const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile(R::MLOG, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  float* sp = sv + p.kb * G::DV;
+  const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1), warp = threadIdx.x >> 5;
+  const int rws = 1 << p.rwlog, kws = kMolWarps >> p.rwlog, rw = warp & (rws - 1), kw = warp >> p.rwlog;
+  const MolTile t = mol_tile(G::WLOG + p.rwlog, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
   if (t.rows <= 0) return;
-  const int own = threadIdx.x / LP;
+  const int own = rw * G::W + lane / LP;
   const bool live = own < t.rows;
-  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const bool warp_live = rw * G::W < t.rows;
   const size_t row = size_t(t.row0) + (live ? own : 0);
   const int kv = p.dk / 4;
-  float4 q[R::KV];
+  float4 q[KV];
 #pragma unroll
-  for (int i = 0; i < R::KV; ++i) {
+  for (int i = 0; i < KV; ++i) {
     const int x = l + LP * i;
     q[i] = x < kv ? load4(static_cast<const T*>(p.a.q) + (row * p.H + head) * p.dk + 4 * x)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -146,22 +146,21 @@ __global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
   const int k_end = min(t.o1, k_begin + per * p.kb);
   for (int k0 = k_begin; k0 < k_end; k0 += p.kb) {
     __syncthreads();
-    stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
+    stage_rows<G::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
                          k0, k_end, sk, sv, sp);
     __syncthreads();
     if (!warp_live) continue;
     const int nk = min(p.kb, k_end - k0);
-    for (int j0 = 0; j0 < nk; j0 += kMolBatch) {
+    for (int j0 = kw * kMolBatch; j0 < nk; j0 += kws * kMolBatch) {
       float s[kMolBatch];
 #pragma unroll
       for (int b = 0; b < kMolBatch; ++b) {
-        float x = 0.f;
+        float x = 0.f, unused;
 #pragma unroll
-        for (int i = 0; i < R::KV; ++i)
+        for (int i = 0; i < KV; ++i)
           if (l + LP * i < kv)
             x = dot4(q[i], *reinterpret_cast<const float4*>(sk + (j0 + b) * p.dk + 4 * (l + LP * i)), x);
         x = group_sum<LP>(x) * p.scale;
-        float unused;
         if (p.cap > 0.f) x = p.cap * mol_tanh(x * p.inv_cap, unused);
         x *= kLog2e;
         if (p.a.slope) {
@@ -185,13 +184,39 @@ __global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
       for (int b = 0; b < kMolBatch; ++b) {
         const float w = fast_exp2(s[b] - ref);
         sum += w;
-        const float* v = sv + (j0 + b) * R::DV + 4 * l;
+        const float* v = sv + (j0 + b) * G::DV + 4 * l;
 #pragma unroll
         for (int i = 0; i < NV; ++i) axpy4(w, *reinterpret_cast<const float4*>(v + 4 * LP * i), o[i]);
       }
     }
   }
-  if (!live) return;
+  // join the warps that shared rows: the first of them adds the others' rows
+  if (kws > 1) {
+    float* oj = msm;                           // [rws][W][DV]
+    float* mj = msm + rws * G::W * G::DV;      // [rws][W][2]
+    const int at = rw * G::W + lane / LP;
+    for (int w = 1; w < kws; ++w) {
+      __syncthreads();
+      if (kw == w) {
+        if (l == 0) mj[2 * at] = mx, mj[2 * at + 1] = sum;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) store4(oj + at * G::DV + 4 * (l + LP * i), o[i]);
+      }
+      __syncthreads();
+      if (kw == 0) {
+        const float m1 = mj[2 * at], up = fmaxf(mx, m1), ref = up == -INFINITY ? 0.f : up;
+        const float f0 = fast_exp2(mx - ref), f1 = fast_exp2(m1 - ref);
+        mx = up;
+        sum = fmaf(sum, f0, f1 * mj[2 * at + 1]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          scale4(f0, o[i]);
+          axpy4(f1, *reinterpret_cast<const float4*>(oj + at * G::DV + 4 * (l + LP * i)), o[i]);
+        }
+      }
+    }
+  }
+  if (!live || kw != 0) return;
   if (p.splits > 1) {
     const size_t at = (size_t(blockIdx.z) * p.nq + row) * p.H + head;
     if (l == 0) {
@@ -212,38 +237,51 @@ __global__ void __launch_bounds__(kMolThreads) mol_fwd_kernel(MolParams p) {
   }
 }
 
-// Joins the key splits: one warp per row and head.
+// Joins the key splits: a block per row and head, whose warps take every fourth
+// split and whose lanes take the columns; the warps' sums are joined in order.
+constexpr int kJoinCols = 32;   // float4 columns at a time
 template <typename T>
-__global__ void mol_join_kernel(MolParams p) {
-  const int lane = threadIdx.x & 31;
-  const size_t rh = (size_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  const size_t total = size_t(p.nq) * p.H;
-  if (rh >= total) return;
-  const size_t row = rh / p.H;
+__global__ void __launch_bounds__(128) mol_join_kernel(MolParams p) {
+  __shared__ float4 part[4][kJoinCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t rh = blockIdx.x, total = size_t(p.nq) * p.H, row = rh / p.H;
   const int head = int(rh - row * p.H);
-  float mx = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[2 * (s * total + rh)]);
+  // maximum and normaliser of up to 64 splits: two a lane
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + rh;
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 a = lane < p.splits ? ml[lane * total] : none, b = lane + 32 < p.splits ? ml[(lane + 32) * total] : none;
+  float mx = fmaxf(a.x, b.x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
-  for (int s = lane; s < p.splits; s += 32) {
-    const float* ml = p.part_ml + 2 * (s * total + rh);
-    sum += ml[1] * fast_exp2(ml[0] - ref);
-  }
+  const float wa = fast_exp2(a.x - ref), wb = fast_exp2(b.x - ref);
+  float sum = fmaf(wa, a.y, wb * b.y);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (lane == 0 && p.lse) p.lse[rh] = sum == 0.f ? -INFINITY : mx * kLn2 + logf(sum);
+  if (threadIdx.x == 0 && p.lse) p.lse[rh] = sum == 0.f ? -INFINITY : mx * kLn2 + logf(sum);
   T* out = static_cast<T*>(p.m) + row * p.D * p.C;
-  for (int x = lane; x < p.dv / 4; x += 32) {
+  const int cols = p.dv / 4;
+  for (int x0 = 0; x0 < cols; x0 += kJoinCols) {
+    const int x = min(x0 + lane, cols - 1);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < p.splits; ++s) {
-      const float w = fast_exp2(p.part_ml[2 * (s * total + rh)] - ref);
+#pragma unroll 4
+    for (int s = warp; s < p.splits; s += 4) {
+      const float w = __shfl_sync(~0u, s < 32 ? wa : wb, s & 31);
       axpy4(w, *reinterpret_cast<const float4*>(p.part_o + (s * total + rh) * p.dv + 4 * x), acc);
     }
-    scale4(inv, acc);
-    store4(out + val_off(p, head, x), acc);
+    __syncthreads();
+    part[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && x0 + lane < cols) {
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 v = part[w][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      scale4(inv, acc);
+      store4(out + val_off(p, head, x), acc);
+    }
   }
 }
 
@@ -264,29 +302,31 @@ __device__ __forceinline__ float pair_weight(const MolParams& p, float x, float 
 }
 
 // dL/dq, the row sums delta, and the query side of dL/dr and dL/dslope.
-template <int NV, int LP, typename T>
+template <int NV, int LP, int KV, typename T>
 __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
-  using R = MolRows<NV, LP>;
+  using G = MolRows<NV, LP>;
   extern __shared__ __align__(16) float msm[];
   float* sk = msm;
   float* sv = sk + p.kb * p.dk;
-  float* sp = sv + p.kb * R::DV;
+  float* sp = sv + p.kb * G::DV;
   __shared__ float warp_ds[kMolWarps];
   const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile(R::MLOG, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  const MolTile t = mol_tile(G::WLOG + p.rwlog, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
   if (t.rows <= 0) {
     if (p.want_pos && threadIdx.x == 0) p.part_ds[size_t(head) * p.slots + blockIdx.x] = 0.f;
     return;
   }
-  const int own = threadIdx.x / LP;
+  const int warp = threadIdx.x >> 5, rws = 1 << p.rwlog, kws = kMolWarps >> p.rwlog;
+  const int rw = warp & (rws - 1), kw = warp >> p.rwlog;
+  const int own = rw * G::W + lane / LP;
   const bool live = own < t.rows;
-  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const bool warp_live = rw * G::W < t.rows;
   const size_t row = size_t(t.row0) + (live ? own : 0);
   const int kv = p.dk / 4;
-  float4 q[R::KV], dq[R::KV], g[NV];
+  float4 q[KV], dq[KV], g[NV];
   float delta = 0.f;
 #pragma unroll
-  for (int i = 0; i < R::KV; ++i) {
+  for (int i = 0; i < KV; ++i) {
     const int x = l + LP * i;
     q[i] = x < kv ? load4(static_cast<const T*>(p.a.q) + (row * p.H + head) * p.dk + 4 * x)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -311,20 +351,20 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
   for (int sweep = p.exact_delta ? 0 : 1; sweep < 2; ++sweep) {
     for (int k0 = t.o0; k0 < t.o1; k0 += p.kb) {
       __syncthreads();
-      stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
+      stage_rows<G::DV, T>(p, head, static_cast<const T*>(p.a.k), static_cast<const T*>(p.a.hp), p.a.posk,
                            k0, t.o1, sk, sv, sp);
       __syncthreads();
       if (!warp_live) continue;
       const int nk = min(p.kb, t.o1 - k0);
-      for (int j = 0; j < nk; ++j) {
+      for (int j = kw; j < nk; j += kws) {
         float x = 0.f, dp = 0.f;
 #pragma unroll
-        for (int i = 0; i < R::KV; ++i)
+        for (int i = 0; i < KV; ++i)
           if (l + LP * i < kv)
             x = dot4(q[i], *reinterpret_cast<const float4*>(sk + j * p.dk + 4 * (l + LP * i)), x);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          dp = dot4(g[i], *reinterpret_cast<const float4*>(sv + j * R::DV + 4 * (l + LP * i)), dp);
+          dp = dot4(g[i], *reinterpret_cast<const float4*>(sv + j * G::DV + 4 * (l + LP * i)), dp);
         x = group_sum<LP>(x);
         dp = group_sum<LP>(dp);
         float d = 0.f, dx = 0.f, dy = 0.f, dz = 0.f, slope_x;
@@ -347,15 +387,49 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
           gz = fmaf(u, dz, gz);
         }
 #pragma unroll
-        for (int i = 0; i < R::KV; ++i)
+        for (int i = 0; i < KV; ++i)
           if (l + LP * i < kv)
             axpy4(ds * slope_x, *reinterpret_cast<const float4*>(sk + j * p.dk + 4 * (l + LP * i)), dq[i]);
       }
     }
+    if (sweep == 0 && kws > 1) {   // the row's delta over the warps that share it
+      const int at = rw * G::W + lane / LP;
+      __syncthreads();
+      if (l == 0) msm[kw * rws * G::W + at] = delta;
+      __syncthreads();
+      delta = 0.f;
+      for (int w = 0; w < kws; ++w) delta += msm[w * rws * G::W + at];
+      __syncthreads();
+    }
   }
-  if (live) {
+  if (kws > 1) {   // and its gradients
+    const int at = rw * G::W + lane / LP;
+    for (int w = 1; w < kws; ++w) {
+      float* oj = msm + at * (p.dk + 4);
+      __syncthreads();
+      if (kw == w) {
 #pragma unroll
-    for (int i = 0; i < R::KV; ++i)
+        for (int i = 0; i < KV; ++i)
+          if (l + LP * i < kv) store4(oj + 4 * (l + LP * i), dq[i]);
+        if (l == 0) store4(oj + p.dk, make_float4(gx, gy, gz, ds_sum));
+      }
+      __syncthreads();
+      if (kw == 0) {
+#pragma unroll
+        for (int i = 0; i < KV; ++i)
+          if (l + LP * i < kv) axpy4(1.f, *reinterpret_cast<const float4*>(oj + 4 * (l + LP * i)), dq[i]);
+        const float4 g = *reinterpret_cast<const float4*>(oj + p.dk);
+        gx += g.x;
+        gy += g.y;
+        gz += g.z;
+        ds_sum += g.w;
+      }
+    }
+  }
+  const bool writer = live && kw == 0;
+  if (writer) {
+#pragma unroll
+    for (int i = 0; i < KV; ++i)
       if (l + LP * i < kv)
         store4(static_cast<T*>(p.g.dq) + (row * p.H + head) * p.dk + 4 * (l + LP * i), dq[i]);
     if (l == 0) {
@@ -369,7 +443,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
     }
   }
   if (p.want_pos) {
-    float v = live && l == 0 ? ds_sum : 0.f;
+    float v = writer && l == 0 ? ds_sum : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     if (lane == 0) warp_ds[threadIdx.x / 32] = v;
@@ -384,25 +458,27 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
 
 // dL/dk, dL/dh' and the key side of dL/dr: a lane group owns a key row and
 // meets the molecule's query rows.
-template <int NV, int LP, typename T>
+template <int NV, int LP, int KV, typename T>
 __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
-  using R = MolRows<NV, LP>;
+  using G = MolRows<NV, LP>;
   extern __shared__ __align__(16) float msm[];
   float* sq = msm;
   float* sg = sq + p.kb * p.dk;
-  float* sp = sg + p.kb * R::DV;
+  float* sp = sg + p.kb * G::DV;
   float* sl = sp + 4 * p.kb;   // lse2, delta
   const int head = blockIdx.y, lane = threadIdx.x & 31, l = lane & (LP - 1);
-  const MolTile t = mol_tile(R::MLOG, p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
+  const MolTile t = mol_tile(G::WLOG + p.rwlog, p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
   if (t.rows <= 0) return;
-  const int own = threadIdx.x / LP;
+  const int warp = threadIdx.x >> 5, rws = 1 << p.rwlog, kws = kMolWarps >> p.rwlog;
+  const int rw = warp & (rws - 1), kw = warp >> p.rwlog;
+  const int own = rw * G::W + lane / LP;
   const bool live = own < t.rows;
-  const bool warp_live = (threadIdx.x & ~31) / LP < t.rows;
+  const bool warp_live = rw * G::W < t.rows;
   const size_t row = size_t(t.row0) + (live ? own : 0);
   const int kv = p.dk / 4;
-  float4 k[R::KV], dk[R::KV], v[NV], dv[NV];
+  float4 k[KV], dk[KV], v[NV], dv[NV];
 #pragma unroll
-  for (int i = 0; i < R::KV; ++i) {
+  for (int i = 0; i < KV; ++i) {
     const int x = l + LP * i;
     k[i] = x < kv ? load4(static_cast<const T*>(p.a.k) + (row * p.H + head) * p.dk + 4 * x)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -423,7 +499,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
   float gx = 0.f, gy = 0.f, gz = 0.f;
   for (int q0 = t.o0; q0 < t.o1; q0 += p.kb) {
     __syncthreads();
-    stage_rows<R::DV, T>(p, head, static_cast<const T*>(p.a.q), static_cast<const T*>(p.g.g), p.a.posq, q0,
+    stage_rows<G::DV, T>(p, head, static_cast<const T*>(p.a.q), static_cast<const T*>(p.g.g), p.a.posq, q0,
                          t.o1, sq, sg, sp);
     for (int i = threadIdx.x; i < p.kb; i += kMolThreads) {
       const bool in = q0 + i < t.o1;
@@ -434,15 +510,15 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
     __syncthreads();
     if (!warp_live) continue;
     const int nq = min(p.kb, t.o1 - q0);
-    for (int j = 0; j < nq; ++j) {
+    for (int j = kw; j < nq; j += kws) {
       float x = 0.f, dp = 0.f;
 #pragma unroll
-      for (int i = 0; i < R::KV; ++i)
+      for (int i = 0; i < KV; ++i)
         if (l + LP * i < kv)
           x = dot4(k[i], *reinterpret_cast<const float4*>(sq + j * p.dk + 4 * (l + LP * i)), x);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        dp = dot4(v[i], *reinterpret_cast<const float4*>(sg + j * R::DV + 4 * (l + LP * i)), dp);
+        dp = dot4(v[i], *reinterpret_cast<const float4*>(sg + j * G::DV + 4 * (l + LP * i)), dp);
       x = group_sum<LP>(x);
       dp = group_sum<LP>(dp);
       float d = 0.f, dx = 0.f, dy = 0.f, dz = 0.f, slope_x;
@@ -461,16 +537,42 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        axpy4(w, *reinterpret_cast<const float4*>(sg + j * R::DV + 4 * (l + LP * i)), dv[i]);
+        axpy4(w, *reinterpret_cast<const float4*>(sg + j * G::DV + 4 * (l + LP * i)), dv[i]);
 #pragma unroll
-      for (int i = 0; i < R::KV; ++i)
+      for (int i = 0; i < KV; ++i)
         if (l + LP * i < kv)
           axpy4(ds * slope_x, *reinterpret_cast<const float4*>(sq + j * p.dk + 4 * (l + LP * i)), dk[i]);
     }
   }
-  if (!live) return;
+  if (kws > 1) {   // the warps that share a row
+    float* oj = msm + (rw * G::W + lane / LP) * (G::DV + p.dk + 4);
+    for (int w = 1; w < kws; ++w) {
+      __syncthreads();
+      if (kw == w) {
 #pragma unroll
-  for (int i = 0; i < R::KV; ++i)
+        for (int i = 0; i < NV; ++i) store4(oj + 4 * (l + LP * i), dv[i]);
+#pragma unroll
+        for (int i = 0; i < KV; ++i)
+          if (l + LP * i < kv) store4(oj + G::DV + 4 * (l + LP * i), dk[i]);
+        if (l == 0) store4(oj + G::DV + p.dk, make_float4(gx, gy, gz, 0.f));
+      }
+      __syncthreads();
+      if (kw == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) axpy4(1.f, *reinterpret_cast<const float4*>(oj + 4 * (l + LP * i)), dv[i]);
+#pragma unroll
+        for (int i = 0; i < KV; ++i)
+          if (l + LP * i < kv) axpy4(1.f, *reinterpret_cast<const float4*>(oj + G::DV + 4 * (l + LP * i)), dk[i]);
+        const float4 g = *reinterpret_cast<const float4*>(oj + G::DV + p.dk);
+        gx += g.x;
+        gy += g.y;
+        gz += g.z;
+      }
+    }
+  }
+  if (!live || kw != 0) return;
+#pragma unroll
+  for (int i = 0; i < KV; ++i)
     if (l + LP * i < kv)
       store4(static_cast<T*>(p.g.dk) + (row * p.H + head) * p.dk + 4 * (l + LP * i), dk[i]);
 #pragma unroll
@@ -554,22 +656,26 @@ int ceil_log2(int x) {
   return l;
 }
 int head_columns(const egat_mol_shape& s) { return (s.lmax + 1) * (s.lmax + 1) * (s.C / s.H); }
-// rows of a generic tile, and a lower bound of it for workspace sizes
-int generic_rows(const egat_mol_shape& s) {
-  int m = 4;
-  by_rows(head_columns(s), [&](auto nv, auto lp) {
-    m = MolRows<decltype(nv)::value, decltype(lp)::value>::M;
-    return 0;
+// ... and the query vectors of a lane
+template <typename F>
+int by_rows_dk(int dv, int dk, F&& f) {
+  return by_rows(dv, [&](auto nv, auto lp) {
+    constexpr int LP = decltype(lp)::value;
+    if constexpr (LP < 8) {
+      if (dk > 16) return f(nv, lp, std::integral_constant<int, 8 / LP>{});
+    }
+    if constexpr (LP < 4) {
+      if (dk > 8) return f(nv, lp, std::integral_constant<int, 4 / LP>{});
+    }
+    return f(nv, lp, std::integral_constant<int, LP < 2 ? 2 : 1>{});
   });
-  return m;
 }
 
-// How the forward pass cuts a shape: rows of a tile and key splits.  Depends on
-// the shape alone.
+// How a pass cuts a shape: rows of a tile and key splits.  Depends on the shape alone.
 struct MolCut {
   bool tc;
   int umma;     // groups of 128 rows of the tcgen05 kernel, 0: not taken
-  int rwlog;    // tensor-core tiles: 16 << rwlog rows
+  int rwlog;    // log2 of the warps side by side over rows
   int rows;     // rows of a tile
   int groups;   // blocks side by side over heads
   int splits;
@@ -577,26 +683,36 @@ struct MolCut {
 long long tile_blocks(int n, int n_mol, int rows, int groups) {
   return ((long long)n / rows + std::min(n_mol, n)) * groups;
 }
-// 64-row tiles read the other side's rows a quarter as often as 16-row tiles,
-// whose four warps share those rows of one row tile instead: taken where two
-// blocks an SM remain and the molecules are that long.
-int tc_rwlog(int n, int n_mol, int groups) {
+// Tiles of four warps' rows read the other side's rows a quarter as often as tiles
+// of one warp's, whose four warps share those rows instead: taken where `enough`
+// blocks remain and the molecules are that long.
+int wide_log(int n, int n_mol, int rows, int groups, int enough) {
   int l = 2;
-  while (l > 0 && (tile_blocks(n, n_mol, 16 << l, groups) < 2 * 148 || (long long)n < (long long)(8 << l) * n_mol))
+  while (l > 0 && (tile_blocks(n, n_mol, rows << l, groups) < enough || (long long)n < (long long)(rows / 2 << l) * n_mol))
     --l;
   return l;
 }
-MolCut tile_cut(const egat_mol_shape& s) {
+MolCut tile_cut(const egat_mol_shape& s, int n) {
   MolCut c{};
   c.tc = mol_tc_supported(s);
   c.groups = c.tc ? s.H / mol_tc_heads(s) : s.H;
-  c.rwlog = c.tc ? tc_rwlog(s.nq, s.n_mol, c.groups) : 0;
-  c.rows = c.tc ? 16 << c.rwlog : generic_rows(s);
   c.splits = 1;
+  if (c.tc) {
+    c.rwlog = wide_log(n, s.n_mol, 16, c.groups, 2 * 148);
+    c.rows = 16 << c.rwlog;
+    return c;
+  }
+  int w = 1;
+  by_rows(head_columns(s), [&](auto nv, auto lp) {
+    w = MolRows<decltype(nv)::value, decltype(lp)::value>::W;
+    return 0;
+  });
+  c.rwlog = wide_log(n, s.n_mol, w, s.H, 4 * 148);
+  c.rows = w << c.rwlog;
   return c;
 }
 MolCut forward_cut(const egat_mol_shape& s) {
-  MolCut c = tile_cut(s);
+  MolCut c = tile_cut(s, s.nq);
   // Long molecules: tcgen05 tiles of 256 rows, or of 128 where those would leave
   // SMs idle.
   if (mol_umma_supported(s) && (long long)s.nq >= 192LL * s.n_mol && s.n_mol > 0 && s.nk >= 192LL * s.n_mol) {
@@ -608,12 +724,14 @@ MolCut forward_cut(const egat_mol_shape& s) {
       return c;
     }
   }
-  // With fewer row tiles than four waves of 148 SMs, each molecule's keys are cut
-  // so that about that many blocks run, but not below 128 keys a part on average.
+  // With fewer row tiles than two blocks an SM, each molecule's keys are cut, but not
+  // below 128 keys a part on average: one wave of three blocks an SM for one molecule
+  // (four are two waves: 45 instead of 37 us for one row against 32,768), finer for
+  // several, whose lengths may differ.
   if (s.n_mol > 0 && s.nk > 0 && c.rwlog == 0) {
     const long long blocks = std::max(1LL, tile_blocks(s.nq, s.n_mol, c.rows, c.groups));
-    const long long most = s.nk / s.n_mol / 128, want = (4LL * 148 + blocks - 1) / blocks;
-    c.splits = int(std::max(1LL, std::min(std::min(most, want), 64LL)));
+    const long long most = s.nk / s.n_mol / 128, want = (s.n_mol > 1 ? 8LL : 3LL) * 148 / blocks;
+    if (blocks < 2 * 148) c.splits = int(std::max(1LL, std::min(std::min(most, want), 64LL)));
   }
   return c;
 }
@@ -639,32 +757,34 @@ MolParams base_params(const egat_mol_shape& s, const MolArgs& a) {
   p.kb = std::max(kMolBatch, std::min(32, int(40 * 1024 / (4 * (s.dk + p.dv + 6))) & ~(kMolBatch - 1)));
   return p;
 }
-size_t stage_bytes(const MolParams& p) { return size_t(p.kb) * (p.dk + p.dv + 6) * sizeof(float); }
+// a staged tile, or the rows that the warps of a tile join
+size_t stage_bytes(const MolParams& p, int w) {
+  return size_t(std::max(p.kb, w << p.rwlog)) * (p.dk + p.dv + 6) * sizeof(float);
+}
 int launched() { return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA; }
 
 template <typename T>
 int forward_t(const MolParams& p, cudaStream_t st) {
-  return by_rows(p.dv, [&](auto nv, auto lp) {
-    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value;
-    mol_fwd_kernel<NV, LP, T><<<dim3(p.slots, p.H, p.splits), kMolThreads, stage_bytes(p), st>>>(p);
-    return launched();
+  return by_rows_dk(p.dv, p.dk, [&](auto nv, auto lp, auto kv) {
+    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value, KV = decltype(kv)::value;
+    return mol_launch(mol_fwd_kernel<NV, LP, KV, T>, dim3(p.slots, p.H, p.splits), kMolThreads,
+                      stage_bytes(p, MolRows<NV, LP>::W), p, st);
   });
 }
 
 template <typename T>
-int backward_t(const MolParams& p, cudaStream_t st) {
-  return by_rows(p.dv, [&](auto nv, auto lp) {
-    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value, M = MolRows<NV, LP>::M;
-    if (p.nq > 0) {
-      mol_bwd_q_kernel<NV, LP, T><<<dim3(p.slots, p.H), kMolThreads, stage_bytes(p), st>>>(p);
-      if (launched() != EGAT_OK) return int(EGAT_ERR_CUDA);
-    }
-    if (p.nk > 0) {
-      const int ks = mol_slots(p.nk, p.nmol, M);
-      mol_bwd_k_kernel<NV, LP, T><<<dim3(ks, p.H), kMolThreads, stage_bytes(p), st>>>(p);
-      if (launched() != EGAT_OK) return int(EGAT_ERR_CUDA);
-    }
-    return int(EGAT_OK);
+int backward_t(MolParams p, int k_rwlog, cudaStream_t st) {
+  return by_rows_dk(p.dv, p.dk, [&](auto nv, auto lp, auto kv) {
+    constexpr int NV = decltype(nv)::value, LP = decltype(lp)::value, KV = decltype(kv)::value;
+    constexpr int W = MolRows<NV, LP>::W;
+    int rc = EGAT_OK;
+    if (p.nq > 0)
+      rc = mol_launch(mol_bwd_q_kernel<NV, LP, KV, T>, dim3(p.slots, p.H), kMolThreads, stage_bytes(p, W), p, st);
+    p.rwlog = k_rwlog;
+    if (rc == EGAT_OK && p.nk > 0)
+      rc = mol_launch(mol_bwd_k_kernel<NV, LP, KV, T>, dim3(mol_slots(p.nk, p.nmol, W << p.rwlog), p.H), kMolThreads,
+                      stage_bytes(p, W), p, st);
+    return rc;
   });
 }
 
@@ -677,7 +797,7 @@ struct MolBwdWs {
 };
 MolBwdWs bwd_ws(const egat_mol_shape& s) {
   MolBwdWs w;
-  w.cut = tile_cut(s);
+  w.cut = tile_cut(s, s.nq);
   w.slots = mol_slots(s.nq, s.n_mol, w.cut.rows);
   w.delta = 0;
   w.nlse2 = up256(sizeof(float) * size_t(s.nq) * s.H);
@@ -723,7 +843,7 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
   const int rc = c.tc ? mol_tc_forward(p, st)
                       : s.dtype == EGAT_BF16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
   if (rc != EGAT_OK || p.splits == 1) return rc;
-  const unsigned blocks = unsigned((size_t(p.nq) * p.H + 3) / 4);
+  const unsigned blocks = unsigned(size_t(p.nq) * p.H);
   if (s.dtype == EGAT_BF16)
     mol_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p);
   else
@@ -753,13 +873,14 @@ int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const Mo
   p.slots = w.slots;
   p.groups = w.cut.groups;
   p.rwlog = w.cut.rwlog;
+  const int k_rwlog = tile_cut(s, s.nk).rwlog;
   int rc = EGAT_OK;
   if (w.cut.tc) {
     if (s.nq > 0) rc = mol_tc_backward_q(p, st);
-    p.rwlog = tc_rwlog(s.nk, s.n_mol, p.groups);
+    p.rwlog = k_rwlog;
     if (rc == EGAT_OK && s.nk > 0) rc = mol_tc_backward_k(p, st);
   } else {
-    rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, st) : backward_t<float>(p, st);
+    rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, k_rwlog, st) : backward_t<float>(p, k_rwlog, st);
   }
   if (rc != EGAT_OK || !p.want_pos) return rc;
   if (s.nq == 0) {   // no query tile ran

@@ -128,4 +128,12 @@ size_t mol_umma_query_bytes(const egat_mol_shape& s, int groups);
 int mol_umma_pack(const MolParams& p, int groups, cudaStream_t st);
 int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st);
 
+template <typename K>
+int mol_launch(K* kernel, dim3 grid, int threads, size_t shm, const MolParams& p, cudaStream_t st) {
+  if (shm > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shm)) != cudaSuccess)
+    return EGAT_ERR_CUDA;
+  kernel<<<grid, threads, shm, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA;
+}
 }  // namespace egat

@@ -377,14 +377,6 @@ int mol_flags(bool a, bool b, F&& f) {
 }
 
 template <typename K>
-int mol_launch(K* kernel, dim3 grid, int threads, size_t shm, const MolParams& p, cudaStream_t st) {
-  if (shm > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shm)) != cudaSuccess)
-    return EGAT_ERR_CUDA;
-  kernel<<<grid, threads, shm, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA;
-}
-template <typename K>
 int tc_launch(K* kernel, dim3 grid, size_t shm, const MolParams& p, cudaStream_t st) {
   return mol_launch(kernel, grid, kTcThreads, shm, p, st);
 }
