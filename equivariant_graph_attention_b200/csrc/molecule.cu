@@ -810,6 +810,19 @@ MolBwdWs bwd_ws(const egat_mol_shape& s) {
 
 }  // namespace
 
+// Two heads a warp where the accumulators of two fit its registers, one of float32.
+int mol_tc_heads(const egat_mol_shape& s) {
+  return s.dtype == EGAT_BF16 && head_columns(s) <= 72 ? 2 : 1;
+}
+// Up to 256 value columns a head of bf16 and 144 of float32 (the accumulators of 16
+// rows and the operands beside them fill a warp's registers there), and two heads
+// where two are taken together.
+bool mol_tc_supported(const egat_mol_shape& s) {
+  const int nt = head_columns(s) / 8;
+  return s.H >= mol_tc_heads(s) && (nt == 1 || nt == 2 || nt == 4 || nt == 8 || nt == 9 || nt == 16 || nt == 18 ||
+                                    (nt == 32 && s.dtype == EGAT_BF16));
+}
+
 size_t molecule_ws_bytes(const egat_mol_shape& s) {
   const MolCut c = forward_cut(s);
   if (c.umma) return up256(mol_umma_key_bytes(s)) + up256(mol_umma_query_bytes(s, c.umma));
@@ -840,11 +853,12 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
                                          up256(size_t(p.splits) * s.nq * s.H * p.dv * sizeof(float)));
   }
   p.slots = mol_slots(s.nq, s.n_mol, c.rows);
-  const int rc = c.tc ? mol_tc_forward(p, st)
-                      : s.dtype == EGAT_BF16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
+  const bool bf16 = s.dtype == EGAT_BF16;
+  const int rc = c.tc ? (bf16 ? mol_tc_forward_bf16(p, st) : mol_tc_forward_f32(p, st))
+                      : bf16 ? forward_t<__nv_bfloat16>(p, st) : forward_t<float>(p, st);
   if (rc != EGAT_OK || p.splits == 1) return rc;
   const unsigned blocks = unsigned(size_t(p.nq) * p.H);
-  if (s.dtype == EGAT_BF16)
+  if (bf16)
     mol_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p);
   else
     mol_join_kernel<float><<<blocks, 128, 0, st>>>(p);
@@ -873,14 +887,15 @@ int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const Mo
   p.slots = w.slots;
   p.groups = w.cut.groups;
   p.rwlog = w.cut.rwlog;
+  const bool bf16 = s.dtype == EGAT_BF16;
   const int k_rwlog = tile_cut(s, s.nk).rwlog;
   int rc = EGAT_OK;
   if (w.cut.tc) {
-    if (s.nq > 0) rc = mol_tc_backward_q(p, st);
+    if (s.nq > 0) rc = bf16 ? mol_tc_backward_q_bf16(p, st) : mol_tc_backward_q_f32(p, st);
     p.rwlog = k_rwlog;
-    if (rc == EGAT_OK && s.nk > 0) rc = mol_tc_backward_k(p, st);
+    if (rc == EGAT_OK && s.nk > 0) rc = bf16 ? mol_tc_backward_k_bf16(p, st) : mol_tc_backward_k_f32(p, st);
   } else {
-    rc = s.dtype == EGAT_BF16 ? backward_t<__nv_bfloat16>(p, k_rwlog, st) : backward_t<float>(p, k_rwlog, st);
+    rc = bf16 ? backward_t<__nv_bfloat16>(p, k_rwlog, st) : backward_t<float>(p, k_rwlog, st);
   }
   if (rc != EGAT_OK || !p.want_pos) return rc;
   if (s.nq == 0) {   // no query tile ran

@@ -113,13 +113,16 @@ __device__ __forceinline__ float mol_sqrt(float x) {
   return r;
 }
 
-// Tensor-core kernels (bf16 storage): value tiles of 8 columns a head they
-// take, and their launches.  rows = rows of a tile, 16 << p.rwlog.
+// Tensor-core kernels in tiles of 16 << p.rwlog rows: whether they take the shape,
+// the heads that a warp takes together, and their launches.
 bool mol_tc_supported(const egat_mol_shape& s);
-int mol_tc_heads(const egat_mol_shape& s);   // heads a warp takes together
-int mol_tc_forward(const MolParams& p, cudaStream_t st);
-int mol_tc_backward_q(const MolParams& p, cudaStream_t st);
-int mol_tc_backward_k(const MolParams& p, cudaStream_t st);
+int mol_tc_heads(const egat_mol_shape& s);
+int mol_tc_forward_bf16(const MolParams& p, cudaStream_t st);
+int mol_tc_forward_f32(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_q_bf16(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_q_f32(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_k_bf16(const MolParams& p, cudaStream_t st);
+int mol_tc_backward_k_f32(const MolParams& p, cudaStream_t st);
 // tcgen05 kernels: whether they take the shape, the sizes of the operand blocks
 // and their packing, and the forward pass in tiles of 128 * groups rows.
 bool mol_umma_supported(const egat_mol_shape& s);

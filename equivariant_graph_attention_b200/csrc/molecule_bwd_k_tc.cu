@@ -1,245 +1,8 @@
-// Attention within each molecule on tensor cores (bf16 storage): the key side
-// of the backward pass.
-#include "molecule_tc.cuh"
+// Attention within each molecule on tensor cores, bf16 storage: the key side of the backward pass.
+#include "molecule_bwd_k_tc.cuh"
 
 namespace egat {
-namespace {
 
-// dL/dk, dL/dh' and, with POS, the key side of dL/dr: a warp owns 16 key rows
-// and meets the molecule's query rows.  The products are transposed (S^T = K Q^T,
-// dP^T = H' G^T), so that the weights and dS land as the A operands of
-// dh' = a^T G and dk = dS^T Q.  A query row past the molecule has lse2 = +inf: no weight.
-template <int NT, int KC, int HP, bool CAP, bool BIAS, bool POS>
-__global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
-  using L = TcLay<NT, KC, HP>;
-  // the key rows' values as A fragments: in registers, or read again for every
-  // step where they would not fit beside the accumulators
-  constexpr bool VREG = NT <= 18;
-  extern __shared__ __align__(128) unsigned char tsm[];
-  const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const MolTile t = mol_tile(4 + p.rwlog, p.a.kptr, p.a.qptr, p.nmol, p.nk, p.nq, blockIdx.x);
-  if (t.rows <= 0) return;
-  const int rw = warp & ((1 << p.rwlog) - 1), kw = warp >> p.rwlog, kws = 4 >> p.rwlog;
-  const int rA = rw * 16 + g, rB = rA + 8;
-  const bool warp_live = rw * 16 < t.rows, lA = rA < t.rows, lB = rB < t.rows;
-  const size_t rowA = size_t(t.row0) + rA, rowB = rowA + 8;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q);
-  const __nv_bfloat16* gm = static_cast<const __nv_bfloat16*>(p.g.g);
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.hp);
-  const uint32_t sbase = tc_smem(tsm);
-  TcLoader<NT, KC, HP> ld;
-  auto load = [&](int r0, int b) {
-    const uint32_t st = sbase + b * L::STAGE;
-    ld.load(st, t.o1 - r0);
-    // minus lse2 and delta of the query rows; no weight past the molecule
-    for (int i = threadIdx.x; i < kTcStage * HP; i += kTcThreads) {
-      const int r = i / HP, h = i % HP, o = L::ROW + (h * 2 * kTcStage + r) * 4;
-      const size_t at = size_t(r0 + r) * p.H + head0 + h;
-      if (r0 + r < t.o1) {
-        tc_cp4(st + o, p.nlse2 + at, true);
-        tc_cp4(st + o + kTcStage * 4, p.delta + at, true);
-      } else {
-        *reinterpret_cast<float*>(tsm + b * L::STAGE + o) = -INFINITY;
-        *reinterpret_cast<float*>(tsm + b * L::STAGE + o + kTcStage * 4) = 0.f;
-      }
-    }
-  };
-  if (t.o0 < t.o1) {
-    ld.init(p, q, gm, p.a.posq, head0, t.o0);
-    load(t.o0, 0);
-  }
-  tc_commit();
-
-  uint32_t kf[HP][KC][2], vf[HP][VREG ? NT : 1][2];
-  f32x2 slope[HP] = {}, px[2] = {}, py[2] = {}, pz[2] = {};
-#pragma unroll
-  for (int h = 0; h < HP; ++h) {
-    tc_frag_qk<KC>(p, static_cast<const __nv_bfloat16*>(p.a.k), rowA, rowB, lA, lB, head0 + h, kf[h]);
-    if constexpr (VREG) tc_frag_val<NT>(p, v, rowA, rowB, lA, lB, head0 + h, vf[h]);
-    if constexpr (BIAS) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
-  }
-  if constexpr (BIAS)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (r ? lB : lA) {
-        const float* x = p.a.posk + (r ? rowB : rowA) * 3;
-        px[r] = f2_set(-x[0]);
-        py[r] = f2_set(-x[1]);
-        pz[r] = f2_set(-x[2]);
-      }
-  const f32x2 c_in = f2_set(CAP ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
-
-  float dk[HP][KC][4] = {}, dv[HP][NT][4] = {};
-  f32x2 gs[2][3] = {};
-  int buf = 0;
-  for (int q0 = t.o0; q0 < t.o1; q0 += kTcStage, buf ^= 1) {
-    if (q0 + kTcStage < t.o1) load(q0 + kTcStage, buf ^ 1);
-    tc_commit();
-    tc_wait<1>();
-    __syncthreads();
-    const uint32_t st = sbase + buf * L::STAGE;
-    const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
-    const float* sl = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::ROW);
-    const int n = min(kTcStage, t.o1 - q0);
-    if (warp_live)
-#pragma unroll 1
-      for (int j = kw * 16; j < n; j += kws * 16) {
-        f32x2 d[2][2] = {}, ri[2][2] = {};
-        if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
-        f32x2 u[2][2] = {};   // POS: sum over the heads of slope dS
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          float s[2][4] = {}, dp[2][4] = {};
-          tc_dot<KC>(s, kf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
-          const uint32_t gb = st + L::VAL + j * L::RV + h * 16;
-          if constexpr (VREG) {
-            tc_dot<NT>(dp, vf[h], gb + tc_lane_n(L::RV, HP * 16), gb + tc_lane_n2(L::RV), HP * 16);
-          } else {
-#pragma unroll 4
-            for (int c = 0; c < NT; c += 2) {
-              uint32_t a[2][2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int o = tc_val_off(p, head0 + h, c + e) + t2;
-                a[e][0] = lA ? __ldg(reinterpret_cast<const uint32_t*>(v + rowA * (p.D * p.C) + o)) : 0u;
-                a[e][1] = lB ? __ldg(reinterpret_cast<const uint32_t*>(v + rowB * (p.D * p.C) + o)) : 0u;
-              }
-              tc_dot<2, true>(dp, a, gb + c * HP * 16 + tc_lane_n(L::RV, HP * 16), 0, HP * 16);
-            }
-          }
-          f32x2 x[4], fx[CAP ? 4 : 1];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[2 * c] = f2_pack(s[c][0], s[c][1]);
-            x[2 * c + 1] = f2_pack(s[c][2], s[c][3]);
-          }
-          if constexpr (CAP) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
-            tc_cap<4, true>(x, fx);
-          }
-          uint32_t fd[2][2], fa[2][2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = i >> 1, r = i & 1;
-            const f32x2* row = reinterpret_cast<const f32x2*>(sl + h * 2 * kTcStage + j + 8 * c + t2);
-            x[i] = f2_fma(x[i], CAP ? c_cap : c_in, row[0]);
-            if constexpr (BIAS) x[i] = f2_fma(d[c][r], slope[h], x[i]);
-            float a, b;
-            f2_unpack(x[i], a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            fa[c][r] = tc_pack(a, b);
-            f32x2 ds = f2_mul(f2_pack(a, b), f2_add(f2_pack(dp[c][2 * r], dp[c][2 * r + 1]), row[kTcStage / 2]));
-            if (POS) u[c][r] = f2_fma(ds, slope[h], u[c][r]);
-            if constexpr (CAP) ds = f2_mul(ds, fx[i]);
-            f2_unpack(ds, a, b);
-            fd[c][r] = tc_pack(a, b);
-          }
-          tc_apply<NT>(dv[h], fa, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16);
-          tc_apply<KC>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16);
-        }
-        if (POS) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
-              const f32x2 f = f2_mul(u[c][r], ri[c][r]);
-#pragma unroll
-              for (int e = 0; e < 3; ++e) gs[r][e] = f2_fma(f, dir[e], gs[r][e]);
-            }
-          }
-        }
-      }
-    __syncthreads();
-  }
-
-  // join the warps that shared rows: dh' first, then dk and the positions
-  constexpr int QN = HP * KC * 8, ROW = QN + (POS ? 3 : 0) + 1;
-  float* oacc = reinterpret_cast<float*>(tsm);            // [4 warps][16][OUTROW]
-  float* o = oacc + 4 * 16 * L::OUTROW;                    // [4 warps][16][ROW]
-  tc_wait<0>();
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = warp * 16 + g + 8 * r;
-#pragma unroll
-    for (int h = 0; h < HP; ++h) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-        *reinterpret_cast<float2*>(oacc + row * L::OUTROW + (x * HP + h) * 8 + t2) =
-            make_float2(dv[h][x][2 * r], dv[h][x][2 * r + 1]);
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) o[row * ROW + (h * KC + c) * 8 + t2 + e] = dk[h][c][2 * r + e];
-    }
-    if constexpr (POS)
-#pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        float g0, g1;
-        f2_unpack(gs[r][e], g0, g1);
-        const float x = quad_sum(g0 + g1);
-        if (t2 == 0) o[row * ROW + QN + e] = x;
-      }
-  }
-  __syncthreads();
-  const int rws = 1 << p.rwlog, kc = p.dk >> 3;
-  for (int i = threadIdx.x; i < t.rows * HP * NT; i += kTcThreads) {
-    const int row = i / (HP * NT), c = i % (HP * NT), x = c / HP, h = c % HP;
-    float s[8] = {};
-    for (int w = 0; w < kws; ++w)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += oacc[(w * rws * 16 + row) * L::OUTROW + c * 8 + e];
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.g.dhp) + (size_t(t.row0) + row) * (p.D * p.C) +
-                              tc_val_off(p, head0 + h, x)) =
-        make_uint4(tc_pack(s[0], s[1]), tc_pack(s[2], s[3]), tc_pack(s[4], s[5]), tc_pack(s[6], s[7]));
-  }
-  auto sum_at = [&](int row, int i) {
-    float x = 0.f;
-    for (int w = 0; w < kws; ++w) x += o[(w * rws * 16 + row) * ROW + i];
-    return x;
-  };
-  for (int i = threadIdx.x; i < t.rows * HP * KC; i += kTcThreads) {
-    const int row = i / (HP * KC), c = i % (HP * KC), h = c / KC, cc = c % KC;
-    if (cc >= kc) continue;
-    uint32_t u[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = tc_pack(p.scale * sum_at(row, c * 8 + 2 * e), p.scale * sum_at(row, c * 8 + 2 * e + 1));
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.g.dk) +
-                              ((size_t(t.row0) + row) * p.H + head0 + h) * p.dk + cc * 8) =
-        make_uint4(u[0], u[1], u[2], u[3]);
-  }
-  if constexpr (POS)
-    for (int i = threadIdx.x; i < t.rows * 3; i += kTcThreads) {
-      const int row = i / 3, e = i % 3;
-      p.part_dk[(size_t(blockIdx.y) * p.nk + t.row0 + row) * 3 + e] = -kLn2 * sum_at(row, QN + e);
-    }
-}
-
-}  // namespace
-
-int mol_tc_backward_k(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
-    constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
-    using L = TcLay<NT, KC, HP>;
-    const size_t join = 4 * 16 * (L::OUTROW + HP * KC * 8 + 4) * 4;
-    const size_t shm = std::max(size_t(2 * L::STAGE), join);
-    const dim3 grid(mol_slots(p.nk, p.nmol, 16 << p.rwlog), p.H / HP);
-    // positions come with a bias
-    if (p.want_pos)
-      return mol_flags(p.cap > 0.f, true, [&](auto cap, auto) {
-        return tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, decltype(cap)::value, true, true>, grid, shm, p, st);
-      });
-    return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
-      return tc_launch(mol_bwd_k_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value, false>, grid, shm, p,
-                       st);
-    });
-  });
-}
+int mol_tc_backward_k_bf16(const MolParams& p, cudaStream_t st) { return tc_backward_k<1>(p, st); }
 
 }  // namespace egat

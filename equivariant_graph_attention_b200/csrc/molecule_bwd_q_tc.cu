@@ -1,306 +1,8 @@
-// Attention within each molecule on tensor cores (bf16 storage): the query side
-// of the backward pass.
-#include "molecule_tc.cuh"
+// Attention within each molecule on tensor cores, bf16 storage: the query side of the backward pass.
+#include "molecule_bwd_q_tc.cuh"
 
 namespace egat {
-namespace {
 
-// dL/dq, the row sums delta_i = sum_j a_ij dP_ij and, with POS, the query side
-// of dL/dr and dL/dslope, in one sweep over the keys.  The sweep takes
-// dS' = a (dP - delta') with delta' = G . m from the stored, rounded m, and sums
-// delta itself in float32 beside it.  Every output is linear in delta:
-//   dq = sum dS' f' k + (delta' - delta) sum a f' k,
-// so the second sum, of weights alone, takes the rounding of m out at the end;
-// the correction is small, so nothing cancels.
-template <int NT, int KC, int HP, bool CAP, bool BIAS, bool POS>
-__global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
-  using L = TcLay<NT, KC, HP>;
-  extern __shared__ __align__(128) unsigned char tsm[];
-  const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const MolTile t = mol_tile(4 + p.rwlog, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
-  if (t.rows <= 0) {
-    if (POS && threadIdx.x < HP) p.part_ds[size_t(head0 + threadIdx.x) * p.slots + blockIdx.x] = 0.f;
-    return;
-  }
-  const int rw = warp & ((1 << p.rwlog) - 1), kw = warp >> p.rwlog, kws = 4 >> p.rwlog;
-  const int rA = rw * 16 + g, rB = rA + 8;
-  const bool warp_live = rw * 16 < t.rows, lA = rA < t.rows, lB = rB < t.rows;
-  const size_t rowA = size_t(t.row0) + rA, rowB = rowA + 8;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.a.k);
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.hp);
-  const uint32_t sbase = tc_smem(tsm);
-  TcLoader<NT, KC, HP> ld;
-  if (t.o0 < t.o1) {
-    ld.init(p, k, v, p.a.posk, head0, t.o0);
-    ld.load(sbase, t.o1 - t.o0);
-  }
-  tc_commit();
-
-  uint32_t qf[HP][KC][2], gf[HP][NT][2];
-  float lse2[HP][2], dlt[HP][2];   // rows that are not there: lse2 = +inf, no weight
-  f32x2 slope[HP] = {}, px[2] = {}, py[2] = {}, pz[2] = {};
-#pragma unroll
-  for (int h = 0; h < HP; ++h) {
-    tc_frag_qk<KC>(p, static_cast<const __nv_bfloat16*>(p.a.q), rowA, rowB, lA, lB, head0 + h, qf[h]);
-    tc_frag_val<NT>(p, static_cast<const __nv_bfloat16*>(p.g.g), rowA, rowB, lA, lB, head0 + h, gf[h]);
-    float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int o = tc_val_off(p, head0 + h, c) + t2;
-      const __nv_bfloat16* m = static_cast<const __nv_bfloat16*>(p.g.m);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t w = (r ? lB : lA) ? __ldg(reinterpret_cast<const uint32_t*>(m + (r ? rowB : rowA) * (p.D * p.C) + o)) : 0u;
-        float a, b, x, y;
-        f2_unpack(bf16x2_to_f2(w), a, b);
-        f2_unpack(bf16x2_to_f2(gf[h][c][r]), x, y);
-        (r ? d1 : d0) += fmaf(a, x, b * y);
-      }
-    }
-    dlt[h][0] = quad_sum(d0);
-    dlt[h][1] = quad_sum(d1);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool ok = r ? lB : lA;
-      const float x = ok ? p.g.lse[(r ? rowB : rowA) * p.H + head0 + h] * kLog2e : INFINITY;
-      lse2[h][r] = x == -INFINITY ? INFINITY : x;
-    }
-    if constexpr (BIAS) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
-  }
-  if constexpr (BIAS)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (r ? lB : lA) {
-        const float* x = p.a.posq + (r ? rowB : rowA) * 3;
-        px[r] = f2_set(-x[0]);
-        py[r] = f2_set(-x[1]);
-        pz[r] = f2_set(-x[2]);
-      }
-  const f32x2 c_in = f2_set(CAP ? p.scale * p.inv_cap : p.scale * kLog2e), c_cap = f2_set(p.cap * kLog2e);
-  f32x2 nlse[HP][2], ndel[HP][2];   // minus lse2 and delta'
-#pragma unroll
-  for (int h = 0; h < HP; ++h)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      nlse[h][r] = f2_set(-lse2[h][r]);
-      ndel[h][r] = f2_set(-dlt[h][r]);
-    }
-
-  float dq[HP][KC][4] = {}, bk[HP][KC][4] = {};
-  f32x2 del[HP][2] = {};
-  // POS: sums over j of (slope dS', slope a) (r_j - r_i) / d and of (dS', a) d
-  f32x2 gs[2][3] = {}, ga[HP][2][3] = {};
-  float sd[HP][2] = {}, sa[HP][2] = {};
-
-  int buf = 0;
-  for (int k0 = t.o0; k0 < t.o1; k0 += kTcStage, buf ^= 1) {
-    if (k0 + kTcStage < t.o1)
-      ld.load(sbase + (buf ^ 1) * L::STAGE, t.o1 - k0 - kTcStage);
-    tc_commit();
-    tc_wait<1>();
-    __syncthreads();
-    const uint32_t st = sbase + buf * L::STAGE;
-    const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
-    const int n = min(kTcStage, t.o1 - k0);
-    if (warp_live)
-#pragma unroll 1
-      for (int j = kw * 16; j < n; j += kws * 16) {
-        f32x2 d[2][2] = {}, ri[2][2] = {};   // distances (and their reciprocals): [8-key tile][row]
-        if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          float s[2][4] = {}, dp[2][4] = {};
-          tc_dot<KC>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
-          const uint32_t vb = st + L::VAL + j * L::RV + h * 16;
-          tc_dot<NT>(dp, gf[h], vb + tc_lane_n(L::RV, HP * 16), vb + tc_lane_n2(L::RV), HP * 16);
-          f32x2 x[4], fx[CAP ? 4 : 1];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[2 * c] = f2_pack(s[c][0], s[c][1]);
-            x[2 * c + 1] = f2_pack(s[c][2], s[c][3]);
-          }
-          if constexpr (CAP) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
-            tc_cap<4, true>(x, fx);
-          }
-          uint32_t fd[2][2], fa[2][2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = i >> 1, r = i & 1;
-            x[i] = f2_fma(x[i], CAP ? c_cap : c_in, nlse[h][r]);
-            if constexpr (BIAS) x[i] = f2_fma(d[c][r], slope[h], x[i]);
-            float a, b;
-            f2_unpack(x[i], a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            if (j + 16 > n) {   // keys past the molecule
-              if (j + 8 * c + t2 >= n) a = 0.f;
-              if (j + 8 * c + t2 + 1 >= n) b = 0.f;
-            }
-            f32x2 w = f2_pack(a, b);
-            const f32x2 dP = f2_pack(dp[c][2 * r], dp[c][2 * r + 1]);
-            del[h][r] = f2_fma(w, dP, del[h][r]);
-            f32x2 ds = f2_mul(w, f2_add(dP, ndel[h][r]));
-            float lo, hi;
-            if (POS) {
-              const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-              const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
-              const f32x2 wr = f2_mul(w, ri[c][r]), dr = f2_mul(f2_mul(ds, slope[h]), ri[c][r]);
-#pragma unroll
-              for (int e = 0; e < 3; ++e) {
-                gs[r][e] = f2_fma(dr, dir[e], gs[r][e]);
-                ga[h][r][e] = f2_fma(wr, dir[e], ga[h][r][e]);
-              }
-              // d may be inf where the weight is zero
-              float d0, d1;
-              f2_unpack(d[c][r], d0, d1);
-              sa[h][r] += (a != 0.f ? a * d0 : 0.f) + (b != 0.f ? b * d1 : 0.f);
-              f2_unpack(ds, lo, hi);
-              sd[h][r] += (lo != 0.f ? lo * d0 : 0.f) + (hi != 0.f ? hi * d1 : 0.f);
-            }
-            if constexpr (CAP) {
-              ds = f2_mul(ds, fx[i]);
-              w = f2_mul(w, fx[i]);
-              f2_unpack(w, a, b);
-            }
-            f2_unpack(ds, lo, hi);
-            fd[c][r] = tc_pack(lo, hi);
-            fa[c][r] = tc_pack(a, b);
-          }
-          const uint32_t kb = st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16);
-#pragma unroll
-          for (int c = 0; c < KC; c += 2) {
-            uint32_t b[4];
-            tc_ldsm4t(kb + c * 16, b);
-            tc_mma16(dq[h][c], fd[0], fd[1], b[0], b[1]);
-            tc_mma16(dq[h][c + 1], fd[0], fd[1], b[2], b[3]);
-            tc_mma16(bk[h][c], fa[0], fa[1], b[0], b[1]);
-            tc_mma16(bk[h][c + 1], fa[0], fa[1], b[2], b[3]);
-          }
-        }
-      }
-    __syncthreads();
-  }
-
-  // Join the warps that shared rows.  A row's floats: dq, sum a f' k (8 KC HP
-  // each), then per head delta, delta' and, with POS, the sums above.
-  constexpr int QN = HP * KC * 8, PER = POS ? 7 : 2, ROW = 2 * QN + HP * PER + (POS ? 3 : 0) + 1;
-  float* o = reinterpret_cast<float*>(tsm);   // [4 warps][16][ROW]
-  tc_wait<0>();
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float* at = o + (warp * 16 + g + 8 * r) * ROW;
-#pragma unroll
-    for (int h = 0; h < HP; ++h) {
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          at[(h * KC + c) * 8 + t2 + e] = dq[h][c][2 * r + e];
-          at[QN + (h * KC + c) * 8 + t2 + e] = bk[h][c][2 * r + e];
-        }
-      float lo, hi;
-      f2_unpack(del[h][r], lo, hi);
-      const float de = quad_sum(lo + hi);
-      float* x = at + 2 * QN + h * PER;
-      if (t2 == 0) x[0] = de, x[1] = dlt[h][r];
-      if constexpr (POS) {
-        const float v0 = quad_sum(sd[h][r]), v1 = quad_sum(sa[h][r]);
-        if (t2 == 0) x[2] = v0, x[3] = v1;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          float g0, g1;
-          f2_unpack(ga[h][r][e], g0, g1);
-          const float v2 = quad_sum(g0 + g1);
-          if (t2 == 0) x[4 + e] = v2;
-        }
-      }
-    }
-    if constexpr (POS)
-#pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        float g0, g1;
-        f2_unpack(gs[r][e], g0, g1);
-        const float v3 = quad_sum(g0 + g1);
-        if (t2 == 0) at[2 * QN + HP * PER + e] = v3;
-      }
-  }
-  __syncthreads();
-  const int rws = 1 << p.rwlog, kc = p.dk >> 3;
-  auto sum_at = [&](int row, int i) {
-    float x = 0.f;
-    for (int w = 0; w < kws; ++w) x += o[(w * rws * 16 + row) * ROW + i];
-    return x;
-  };
-  for (int i = threadIdx.x; i < t.rows * HP * KC; i += kTcThreads) {
-    const int row = i / (HP * KC), c = i % (HP * KC), h = c / KC, cc = c % KC;
-    if (cc >= kc) continue;
-    const int x = 2 * QN + h * PER;
-    const float eps = o[row * ROW + x + 1] - sum_at(row, x);
-    uint32_t u[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = tc_pack(p.scale * fmaf(eps, sum_at(row, QN + c * 8 + 2 * e), sum_at(row, c * 8 + 2 * e)),
-                     p.scale * fmaf(eps, sum_at(row, QN + c * 8 + 2 * e + 1), sum_at(row, c * 8 + 2 * e + 1)));
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.g.dq) +
-                              ((size_t(t.row0) + row) * p.H + head0 + h) * p.dk + cc * 8) =
-        make_uint4(u[0], u[1], u[2], u[3]);
-  }
-  for (int i = threadIdx.x; i < t.rows * HP; i += kTcThreads) {
-    const int row = i / HP, h = i % HP;
-    const size_t at = (size_t(t.row0) + row) * p.H + head0 + h;
-    const float x = p.g.lse[at] * kLog2e;
-    p.delta[at] = -sum_at(row, 2 * QN + h * PER);
-    p.nlse2[at] = x == -INFINITY ? -INFINITY : -x;   // a row without weights stays without
-  }
-  if constexpr (POS) {
-    // positions: slope here is -slope log2 e, and the directions point from i to j:
-    //   dL/dr_i = sum slope dS (r_j - r_i) / d
-    for (int i = threadIdx.x; i < t.rows * 3; i += kTcThreads) {
-      const int row = i / 3, e = i % 3;
-      float x = -kLn2 * sum_at(row, 2 * QN + HP * PER + e);
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        const int at = 2 * QN + h * PER;
-        x = fmaf(p.a.slope[head0 + h] * (o[row * ROW + at + 1] - sum_at(row, at)), sum_at(row, at + 4 + e), x);
-      }
-      p.part_dq[(size_t(blockIdx.y) * p.nq + t.row0 + row) * 3 + e] = x;
-    }
-    if (warp < HP) {
-      float x = 0.f;
-      for (int row = lane; row < t.rows; row += 32) {
-        const int at = 2 * QN + warp * PER;
-        x -= fmaf(o[row * ROW + at + 1] - sum_at(row, at), sum_at(row, at + 3), sum_at(row, at + 2));
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(~0u, x, s);
-      if (lane == 0) p.part_ds[size_t(head0 + warp) * p.slots + blockIdx.x] = x;
-    }
-  }
-}
-
-}  // namespace
-
-int mol_tc_backward_q(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
-    constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
-    using L = TcLay<NT, KC, HP>;
-    const size_t join = 4 * 16 * (2 * HP * KC * 8 + HP * 7 + 4) * 4;
-    const size_t shm = std::max(size_t(2 * L::STAGE), join);
-    const dim3 grid(p.slots, p.H / HP);
-    // positions come with a bias
-    if (p.want_pos)
-      return mol_flags(p.cap > 0.f, true, [&](auto cap, auto) {
-        return tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, decltype(cap)::value, true, true>, grid, shm, p, st);
-      });
-    return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
-      return tc_launch(mol_bwd_q_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value, false>, grid, shm, p,
-                       st);
-    });
-  });
-}
+int mol_tc_backward_q_bf16(const MolParams& p, cudaStream_t st) { return tc_backward_q<1>(p, st); }
 
 }  // namespace egat

@@ -1,5 +1,6 @@
-// Attention within each molecule on tensor cores (bf16 storage): the forward
-// pass, and the rules of the tensor-core path.
+// Attention within each molecule on tensor cores: the forward pass.
+#pragma once
+
 #include "molecule_tc.cuh"
 
 namespace egat {
@@ -7,13 +8,14 @@ namespace {
 
 // Per 16 x 16 pairs and head: S = Q K^T (one k-step of 16, two at dk 32), base-2
 // scores in packed float32 pairs, the online softmax, and m += P H' with P
-// rounded once to bf16 (the normaliser adds the unrounded weights).  A row's
+// rounded once to bf16 (bf16 storage; the normaliser adds the unrounded weights).  A row's
 // reference moves only when a score passes it by 2^8, so most steps need no
 // exchange between lanes and no rescaling; the rare step that moves it works its
 // scores out again, which keeps them out of the registers in between.
-template <int NT, int KC, int HP, bool CAP, bool BIAS>
+template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kernel(MolParams p) {
-  using L = TcLay<NT, KC, HP>;
+  using L = TcLay<NT, KC, HP, PL>;
+  using T = typename L::T;
   extern __shared__ __align__(128) unsigned char tsm[];
   const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -23,25 +25,22 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   const int rA = rw * 16 + g, rB = rA + 8;
   const bool warp_live = rw * 16 < t.rows, lA = rA < t.rows, lB = rB < t.rows;
   const size_t rowA = size_t(t.row0) + rA, rowB = rowA + 8;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q);
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.a.k);
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.a.hp);
 
   // this split's share of the molecule's stages
   const int stages = (t.o1 - t.o0 + kTcStage - 1) / kTcStage, per = (stages + p.splits - 1) / p.splits;
   const int k_begin = t.o0 + int(blockIdx.z) * per * kTcStage;
   const int k_end = min(t.o1, k_begin + per * kTcStage);
   const uint32_t sbase = tc_smem(tsm);
-  TcLoader<NT, KC, HP> ld;
+  TcLoader<NT, KC, HP, PL> ld;
   if (k_begin < k_end) {
-    ld.init(p, k, v, p.a.posk, head0, k_begin);
-    ld.load(sbase, k_end - k_begin);
+    ld.init(p, p.a.k, p.a.hp, p.a.posk, head0, k_begin);
+    if (L::BUFS == 2) ld.load(sbase, k_end - k_begin);
   }
   tc_commit();
 
-  uint32_t qf[HP][KC][2];
+  uint32_t qf[HP][PL][KC][2];
 #pragma unroll
-  for (int h = 0; h < HP; ++h) tc_frag_qk<KC>(p, q, rowA, rowB, lA, lB, head0 + h, qf[h]);
+  for (int h = 0; h < HP; ++h) tc_frag_qk<KC, PL>(p, p.a.q, rowA, rowB, lA, lB, head0 + h, qf[h]);
   f32x2 px[2] = {}, py[2] = {}, pz[2] = {}, slope[HP] = {};   // minus the rows' positions
   if constexpr (BIAS) {
 #pragma unroll
@@ -65,11 +64,13 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   for (int h = 0; h < HP; ++h) ref[h][0] = ref[h][1] = f2_set(__int_as_float(0x7fffffff));
 
   int buf = 0;
-  for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= 1) {
-    if (k0 + kTcStage < k_end)
+  for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= L::BUFS - 1) {
+    if (L::BUFS == 1)
+      ld.load(sbase, k_end - k0);
+    else if (k0 + kTcStage < k_end)
       ld.load(sbase + (buf ^ 1) * L::STAGE, k_end - k0 - kTcStage);
     tc_commit();
-    tc_wait<1>();
+    tc_wait<L::BUFS - 1>();
     __syncthreads();
     const uint32_t st = sbase + buf * L::STAGE;
     const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
         // base-2 scores of head h plus (n0, n1) by row: w[8-key tile][row]
         auto scores = [&](int h, f32x2 n0, f32x2 n1, f32x2 (&w)[4]) {
           float s[2][4] = {};
-          tc_dot<KC>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16);
+          tc_dot<KC, PL>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16, L::PK);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             w[2 * c] = f2_pack(s[c][0], s[c][1]);
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
         }
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          uint32_t pf[2][2];
+          uint32_t pf[PL][2][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a, b;
@@ -166,9 +167,10 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
             a = fast_exp2(a);
             b = fast_exp2(b);
             sum[h][i & 1] = f2_add(sum[h][i & 1], f2_pack(a, b));
-            pf[i >> 1][i & 1] = tc_pack(a, b);
+            tc_put<PL>(pf, i >> 1, i & 1, a, b);
           }
-          tc_apply<NT>(acc[h], pf, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16);
+          tc_apply<NT, PL>(acc[h], pf, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16,
+                           L::PV);
         }
       }
     __syncthreads();
@@ -227,39 +229,24 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (x == 0 && p.lse) p.lse[rh] = l == 0.f ? -INFINITY : top * kLn2 + logf(l);
-    uint4 u;
-    u.x = tc_pack(o[0] * inv, o[1] * inv);
-    u.y = tc_pack(o[2] * inv, o[3] * inv);
-    u.z = tc_pack(o[4] * inv, o[5] * inv);
-    u.w = tc_pack(o[6] * inv, o[7] * inv);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.m) + at * (p.D * p.C) + tc_val_off(p, head0 + h, x)) = u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    tc_store8(static_cast<T*>(p.m) + at * (p.D * p.C) + tc_val_off(p, head0 + h, x), o);
   }
 }
 
-int value_tiles(const egat_mol_shape& s) { return (s.lmax + 1) * (s.lmax + 1) * (s.C / s.H) / 8; }
-
-}  // namespace
-
-int mol_tc_heads(const egat_mol_shape& s) { return value_tiles(s) <= 9 ? 2 : 1; }
-
-// bf16 rows with up to 256 value columns a head (the accumulators of 16 rows fill
-// half of a warp's registers there), and two heads where two are taken together.
-bool mol_tc_supported(const egat_mol_shape& s) {
-  const int nt = value_tiles(s);
-  return s.dtype == EGAT_BF16 && s.H >= mol_tc_heads(s) &&
-         (nt == 1 || nt == 2 || nt == 4 || nt == 8 || nt == 9 || nt == 16 || nt == 18 || nt == 32);
-}
-
-int mol_tc_forward(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
+template <int PL>
+int tc_forward(const MolParams& p, cudaStream_t st) {
+  return tc_dispatch<PL>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
-    using L = TcLay<NT, KC, HP>;
-    const size_t shm = std::max(2 * L::STAGE, 4 * 16 * (L::OUTROW + 2 * HP) * 4);
+    using L = TcLay<NT, KC, HP, PL>;
+    const size_t shm = std::max(L::BUFS * L::STAGE, 4 * 16 * (L::OUTROW + 2 * HP) * 4);
     const dim3 grid(p.slots, p.H / HP, p.splits);
     return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
-      return tc_launch(mol_fwd_tc_kernel<NT, KC, HP, decltype(cap)::value, decltype(bias)::value>, grid, shm, p, st);
+      return tc_launch(mol_fwd_tc_kernel<NT, KC, HP, PL, decltype(cap)::value, decltype(bias)::value>, grid, shm, p, st);
     });
   });
 }
 
+}  // namespace
 }  // namespace egat

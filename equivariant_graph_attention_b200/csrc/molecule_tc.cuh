@@ -1,5 +1,4 @@
-// Building blocks of the tensor-core kernels of the attention within
-// molecules (bf16 storage).
+// Building blocks of the tensor-core kernels of the attention within molecules.
 //
 // A CTA has four warps; a warp owns 16 rows and HP heads of them, and meets the
 // other side's rows 16 at a time from shared-memory stages of 64 rows.  The
@@ -15,6 +14,14 @@
 // number of chunks, so that the eight rows of an 8 x 8 ldmatrix hit different
 // banks.  Rows past the molecule are zero-filled: NaN of a neighbour cannot
 // enter a product.
+//
+// float32 storage takes the same kernels with PL = 3 planes: every operand, the
+// weights and dS too, is the sum of three bf16 numbers (24 bits), and a product is
+// the six bf16 products whose planes add up to two at most; what is left out is
+// below 2^-25 of the terms.  Six products at the tensor rate are four thirds of the
+// FMA pipe's rate, without its shared-memory reads (216-water box: 107 us on that
+// pipe).  These stages are converted on their way in, so they are not copied
+// asynchronously, and a warp takes one head.
 #pragma once
 
 #include "molecule.cuh"
@@ -25,15 +32,24 @@ namespace {
 constexpr int kTcThreads = 128;
 constexpr int kTcStage = 64;   // rows of a stage
 
-template <int NT, int KC, int HP>
+template <int PL>
+struct TcStorage { using T = __nv_bfloat16; };
+template <>
+struct TcStorage<3> { using T = float; };
+
+template <int NT, int KC, int HP, int PL>
 struct TcLay {
-  static constexpr int RK = ((HP * KC) | 1) * 16;    // bytes of a staged query/key row
-  static constexpr int RV = ((HP * NT) | 1) * 16;    // bytes of a staged value row
+  using T = typename TcStorage<PL>::T;
+  static_assert(PL == 1 || (PL == 3 && HP == 1), "float32: three planes, one head");
+  static constexpr int PK = HP * KC * 16, PV = HP * NT * 16;   // bytes of a row's plane
+  static constexpr int RK = (HP * KC * PL | 1) * 16;           // bytes of a staged query/key row
+  static constexpr int RV = (HP * NT * PL | 1) * 16;           // bytes of a staged value row
   static constexpr int QK = 0;
   static constexpr int VAL = QK + kTcStage * RK;
   static constexpr int POS = VAL + kTcStage * RV;    // x[64], y[64], z[64]
   static constexpr int ROW = POS + kTcStage * 12;    // per head: lse2[64], delta[64]
   static constexpr int STAGE = ROW + HP * kTcStage * 8;
+  static constexpr int BUFS = PL == 1 ? 2 : 1;       // asynchronous copies alone need two stages
   static constexpr int OUTROW = HP * NT * 8 + 8;     // floats of a joined row (bank spread)
 };
 
@@ -90,6 +106,18 @@ __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// (a, b) as pairs of the PL planes
+template <int PL>
+__device__ __forceinline__ void tc_planes(float a, float b, uint32_t (&w)[PL]) {
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    w[i] = tc_pack(a, b);
+    if (i + 1 < PL) {
+      a -= __uint_as_float(w[i] << 16);
+      b -= __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
 __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -117,18 +145,20 @@ __device__ __forceinline__ int tc_val_off(const MolParams& p, int h, int x) {
   return (x >> p.ch8log) * p.C + h * p.ch + ((x & ((1 << p.ch8log) - 1)) << 3);
 }
 
-// Copies consecutive stages of 64 rows of heads head0.. asynchronously.  A row's W
-// chunks are copied by W lanes, 32 / W rows at a time, so a lane keeps its chunk and
-// advances by whole rows.  Rows from `end` on arrive as zeros.
-template <int W>
+// Copies consecutive stages of 64 rows of heads head0...  A row's W chunks are
+// copied by W lanes, 32 / W rows at a time, so a lane keeps its chunk and advances
+// by whole rows.  Rows from `end` on arrive as zeros.
+template <int W, int PL>
 struct TcPart {
+  using T = typename TcStorage<PL>::T;
   static_assert(W <= 32, "a row's chunks are one warp's");
-  static constexpr int ROWS = 32 / W, STEP = ROWS * (kTcThreads / 32), ITS = kTcStage / STEP;
-  const __nv_bfloat16* src;   // this lane's chunk of its first row
-  int ld;                     // elements from row to row
+  static constexpr int ROWS = 32 / W, STEP = ROWS * (kTcThreads / 32), ITS = (kTcStage + STEP - 1) / STEP;
+  static_assert(PL == 3 || kTcStage % STEP == 0, "");
+  const T* src;   // this lane's chunk of its first row
+  int ld;         // elements from row to row
   uint32_t dst;
-  int row;                    // its first row in a stage; past the stage: nothing to copy
-  __device__ __forceinline__ void init(const __nv_bfloat16* base, int ld_, int off, int r0, uint32_t at, int rs) {
+  int row;        // its first row in a stage; past the stage: nothing to copy
+  __device__ __forceinline__ void init(const T* base, int ld_, int off, int r0, uint32_t at, int rs) {
     const int lane = threadIdx.x & 31, r = (threadIdx.x >> 5) * ROWS + lane / W;
     row = lane < ROWS * W ? r : kTcStage;
     ld = ld_;
@@ -137,35 +167,65 @@ struct TcPart {
   }
   template <int RS>
   __device__ __forceinline__ void load(uint32_t st, int left, bool have) {
-    if (row < kTcStage) {
-      if (left >= kTcStage && have) {
+    if constexpr (PL == 1) {
+      if (row < kTcStage) {
+        if (left >= kTcStage && have) {
 #pragma unroll
-        for (int i = 0; i < ITS; ++i) tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
-      } else {
+          for (int i = 0; i < ITS; ++i) tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
+        } else {
 #pragma unroll 1
-        for (int i = 0; i < ITS; ++i) {
-          const bool ok = have && row + i * STEP < left;
-          tc_cp16(st + dst + i * STEP * RS, ok ? src + size_t(i) * STEP * ld : src - size_t(row) * ld, ok);
+          for (int i = 0; i < ITS; ++i) {
+            const bool ok = have && row + i * STEP < left;
+            tc_cp16(st + dst + i * STEP * RS, ok ? src + size_t(i) * STEP * ld : src - size_t(row) * ld, ok);
+          }
+        }
+      }
+    } else {
+      constexpr int AT_ONCE = ITS < 4 ? ITS : 4;   // rows on their way together
+#pragma unroll 1
+      for (int i0 = 0; i0 < ITS; i0 += AT_ONCE) {
+        float4 v[AT_ONCE][2];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+          const bool ok = have && row + (i0 + i) * STEP < min(left, kTcStage);
+          const float4* x = reinterpret_cast<const float4*>(src + size_t(i0 + i) * STEP * ld);
+          v[i][0] = ok ? __ldg(x) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[i][1] = ok ? __ldg(x + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+          if (row + (i0 + i) * STEP >= kTcStage) continue;
+          uint32_t w[4][PL];
+          tc_planes<PL>(v[i][0].x, v[i][0].y, w[0]);
+          tc_planes<PL>(v[i][0].z, v[i][0].w, w[1]);
+          tc_planes<PL>(v[i][1].x, v[i][1].y, w[2]);
+          tc_planes<PL>(v[i][1].z, v[i][1].w, w[3]);
+#pragma unroll
+          for (int k = 0; k < PL; ++k)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(st + dst + (i0 + i) * STEP * RS + k * W * 16),
+                         "r"(w[0][k]), "r"(w[1][k]), "r"(w[2][k]), "r"(w[3][k])
+                         : "memory");
         }
       }
     }
     src += size_t(kTcStage) * ld;
   }
 };
-template <int NT, int KC, int HP>
+template <int NT, int KC, int HP, int PL>
 struct TcLoader {
-  using L = TcLay<NT, KC, HP>;
-  TcPart<HP * KC> qk;
-  TcPart<HP * NT> val;
+  using L = TcLay<NT, KC, HP, PL>;
+  using T = typename L::T;
+  TcPart<HP * KC, PL> qk;
+  TcPart<HP * NT, PL> val;
   const float* pos;
   bool have;   // at dk 8 the second chunk is zeros
   // the first stage starts at row r0 (r0 < end)
-  __device__ __forceinline__ void init(const MolParams& p, const __nv_bfloat16* q, const __nv_bfloat16* v,
-                                       const float* positions, int head0, int r0) {
+  __device__ __forceinline__ void init(const MolParams& p, const void* q, const void* v, const float* positions,
+                                       int head0, int r0) {
     const int lane = threadIdx.x & 31, cq = lane % (HP * KC), cv = lane % (HP * NT);
     have = (cq % KC) * 8 < p.dk;
-    qk.init(q, p.H * p.dk, (head0 + cq / KC) * p.dk + (have ? cq % KC : 0) * 8, r0, L::QK, L::RK);
-    val.init(v, p.D * p.C, tc_val_off(p, head0 + cv % HP, cv / HP), r0, L::VAL, L::RV);
+    qk.init(static_cast<const T*>(q), p.H * p.dk, (head0 + cq / KC) * p.dk + (have ? cq % KC : 0) * 8, r0, L::QK, L::RK);
+    val.init(static_cast<const T*>(v), p.D * p.C, tc_val_off(p, head0 + cv % HP, cv / HP), r0, L::VAL, L::RV);
     pos = p.a.slope ? positions + size_t(r0) * 3 : nullptr;
   }
   __device__ __forceinline__ void load(uint32_t st, int left) {
@@ -182,82 +242,137 @@ struct TcLoader {
   }
 };
 
+// Two elements as pairs of the planes
+__device__ __forceinline__ void tc_load2(const __nv_bfloat16* x, bool ok, uint32_t (&w)[1]) {
+  w[0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(x)) : 0u;
+}
+__device__ __forceinline__ void tc_load2(const float* x, bool ok, uint32_t (&w)[3]) {
+  const float2 v = ok ? __ldg(reinterpret_cast<const float2*>(x)) : make_float2(0.f, 0.f);
+  tc_planes<3>(v.x, v.y, w);
+}
+// ... and as float32
+__device__ __forceinline__ float2 tc_float2(const __nv_bfloat16* x, bool ok) {
+  float2 v;
+  f2_unpack(bf16x2_to_f2(ok ? __ldg(reinterpret_cast<const uint32_t*>(x)) : 0u), v.x, v.y);
+  return v;
+}
+__device__ __forceinline__ float2 tc_float2(const float* x, bool ok) {
+  return ok ? __ldg(reinterpret_cast<const float2*>(x)) : make_float2(0.f, 0.f);
+}
+// Eight elements of a row
+__device__ __forceinline__ void tc_store8(__nv_bfloat16* x, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(x) =
+      make_uint4(tc_pack(v[0], v[1]), tc_pack(v[2], v[3]), tc_pack(v[4], v[5]), tc_pack(v[6], v[7]));
+}
+__device__ __forceinline__ void tc_store8(float* x, const float (&v)[8]) {
+  reinterpret_cast<float4*>(x)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(x)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // A fragments of this lane's rows (r0 = row g, r1 = row g + 8) from global memory
-template <int KC>
-__device__ __forceinline__ void tc_frag_qk(const MolParams& p, const __nv_bfloat16* x, size_t r0, size_t r1, bool l0,
-                                           bool l1, int head, uint32_t (&f)[KC][2]) {
+template <int KC, int PL>
+__device__ __forceinline__ void tc_frag_qk(const MolParams& p, const void* src, size_t r0, size_t r1, bool l0, bool l1,
+                                           int head, uint32_t (&f)[PL][KC][2]) {
+  const typename TcStorage<PL>::T* x = static_cast<const typename TcStorage<PL>::T*>(src);
   const int kc = p.dk >> 3, t2 = (threadIdx.x & 3) * 2;
 #pragma unroll
-  for (int c = 0; c < KC; ++c) {
-    f[c][0] = l0 && c < kc ? __ldg(reinterpret_cast<const uint32_t*>(x + (r0 * p.H + head) * p.dk + c * 8 + t2)) : 0u;
-    f[c][1] = l1 && c < kc ? __ldg(reinterpret_cast<const uint32_t*>(x + (r1 * p.H + head) * p.dk + c * 8 + t2)) : 0u;
-  }
+  for (int c = 0; c < KC; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t w[PL];
+      tc_load2(x + ((r ? r1 : r0) * p.H + head) * p.dk + c * 8 + t2, (r ? l1 : l0) && c < kc, w);
+#pragma unroll
+      for (int k = 0; k < PL; ++k) f[k][c][r] = w[k];
+    }
 }
-template <int NT>
-__device__ __forceinline__ void tc_frag_val(const MolParams& p, const __nv_bfloat16* x, size_t r0, size_t r1, bool l0,
-                                            bool l1, int head, uint32_t (&f)[NT][2]) {
+template <int NT, int PL>
+__device__ __forceinline__ void tc_frag_val(const MolParams& p, const void* src, size_t r0, size_t r1, bool l0, bool l1,
+                                            int head, uint32_t (&f)[PL][NT][2], int c0 = 0) {
+  const typename TcStorage<PL>::T* x = static_cast<const typename TcStorage<PL>::T*>(src);
   const int t2 = (threadIdx.x & 3) * 2;
 #pragma unroll
-  for (int c = 0; c < NT; ++c) {
-    const int o = tc_val_off(p, head, c) + t2;
-    f[c][0] = l0 ? __ldg(reinterpret_cast<const uint32_t*>(x + r0 * (p.D * p.C) + o)) : 0u;
-    f[c][1] = l1 ? __ldg(reinterpret_cast<const uint32_t*>(x + r1 * (p.D * p.C) + o)) : 0u;
-  }
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t w[PL];
+      tc_load2(x + (r ? r1 : r0) * (p.D * p.C) + tc_val_off(p, head, c0 + c) + t2, r ? l1 : l0, w);
+#pragma unroll
+      for (int k = 0; k < PL; ++k) f[k][c][r] = w[k];
+    }
 }
 
 // acc (16 rows x 16 other rows) = (or, with ADD, +=) A (16 rows x NC chunks) . (other rows)^T:
 // base is the lane's address of chunk 0 for a non-transposed x4 load (rows by
 // lane & 7 and lane / 16, chunk by bit 3), base2 that of an x2 load of a last odd
-// chunk; step: bytes from a chunk to the next.
-template <int NC, bool ADD = false>
-__device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[NC][2], uint32_t base, uint32_t base2,
-                                       int step) {
-  static_assert(NC > 1 || !ADD, "");
-  if constexpr (NC == 1) {
-    uint32_t b0, b1;
-    tc_ldsm2(base2, b0, b1);
+// chunk; step and plane: bytes from a chunk, a plane to the next.
+template <int NC, int PL, bool ADD = false>
+__device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[PL][NC][2], uint32_t base, uint32_t base2,
+                                       int step, int plane) {
+  if constexpr (NC == 1 && !ADD) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.f;
-    tc_mma8(acc[0], a[0], b0);
-    tc_mma8(acc[1], a[0], b1);
-    return;
   }
 #pragma unroll
-  for (int c = 0; c + 1 < NC; c += 2) {
-    uint32_t b[4];
-    tc_ldsm4(base + c * step, b);
-    if (c == 0 && !ADD) {
-      tc_mma16_first(acc[0], a[c], a[c + 1], b[0], b[1]);
-      tc_mma16_first(acc[1], a[c], a[c + 1], b[2], b[3]);
-    } else {
-      tc_mma16(acc[0], a[c], a[c + 1], b[0], b[1]);
-      tc_mma16(acc[1], a[c], a[c + 1], b[2], b[3]);
+  for (int q = 0; q < PL; ++q) {
+#pragma unroll
+    for (int c = 0; c + 1 < NC; c += 2) {
+      uint32_t b[4];
+      tc_ldsm4(base + q * plane + c * step, b);
+#pragma unroll
+      for (int k = 0; k < PL - q; ++k) {
+        if (c == 0 && q == 0 && k == 0 && !ADD) {
+          tc_mma16_first(acc[0], a[k][c], a[k][c + 1], b[0], b[1]);
+          tc_mma16_first(acc[1], a[k][c], a[k][c + 1], b[2], b[3]);
+        } else {
+          tc_mma16(acc[0], a[k][c], a[k][c + 1], b[0], b[1]);
+          tc_mma16(acc[1], a[k][c], a[k][c + 1], b[2], b[3]);
+        }
+      }
     }
-  }
-  if constexpr (NC & 1) {
-    uint32_t b0, b1;
-    tc_ldsm2(base2 + (NC - 1) * step, b0, b1);
-    tc_mma8(acc[0], a[NC - 1], b0);
-    tc_mma8(acc[1], a[NC - 1], b1);
+    if constexpr (NC & 1) {
+      uint32_t b0, b1;
+      tc_ldsm2(base2 + q * plane + (NC - 1) * step, b0, b1);
+#pragma unroll
+      for (int k = 0; k < PL - q; ++k) {
+        tc_mma8(acc[0], a[k][NC - 1], b0);
+        tc_mma8(acc[1], a[k][NC - 1], b1);
+      }
+    }
   }
 }
 // acc[NC chunks of columns] += w (16 rows x 16 other rows) . other rows; base is
 // the lane's address of chunk 0 for a transposed x4 load (row by lane & 15,
 // chunk by lane / 16).
-template <int NC>
-__device__ __forceinline__ void tc_apply(float (&acc)[NC][4], const uint32_t (&w)[2][2], uint32_t base, int step) {
+template <int NC, int PL>
+__device__ __forceinline__ void tc_apply(float (&acc)[NC][4], const uint32_t (&w)[PL][2][2], uint32_t base, int step,
+                                         int plane) {
 #pragma unroll
-  for (int c = 0; c + 1 < NC; c += 2) {
-    uint32_t b[4];
-    tc_ldsm4t(base + c * step, b);
-    tc_mma16(acc[c], w[0], w[1], b[0], b[1]);
-    tc_mma16(acc[c + 1], w[0], w[1], b[2], b[3]);
+  for (int q = 0; q < PL; ++q) {
+#pragma unroll
+    for (int c = 0; c + 1 < NC; c += 2) {
+      uint32_t b[4];
+      tc_ldsm4t(base + q * plane + c * step, b);
+#pragma unroll
+      for (int k = 0; k < PL - q; ++k) {
+        tc_mma16(acc[c], w[k][0], w[k][1], b[0], b[1]);
+        tc_mma16(acc[c + 1], w[k][0], w[k][1], b[2], b[3]);
+      }
+    }
+    if constexpr (NC & 1) {
+      uint32_t b0, b1;
+      tc_ldsm2t(base + q * plane + (NC - 1) * step, b0, b1);
+#pragma unroll
+      for (int k = 0; k < PL - q; ++k) tc_mma16(acc[NC - 1], w[k][0], w[k][1], b0, b1);
+    }
   }
-  if constexpr (NC & 1) {
-    uint32_t b0, b1;
-    tc_ldsm2t(base + (NC - 1) * step, b0, b1);
-    tc_mma16(acc[NC - 1], w[0], w[1], b0, b1);
-  }
+}
+// (a, b), columns 2t and 2t + 1 of 8-row tile c and row r, into A fragments
+template <int PL>
+__device__ __forceinline__ void tc_put(uint32_t (&f)[PL][2][2], int c, int r, float a, float b) {
+  uint32_t w[PL];
+  tc_planes<PL>(a, b, w);
+#pragma unroll
+  for (int k = 0; k < PL; ++k) f[k][c][r] = w[k];
 }
 // Lane offsets of those loads inside a stage part with rows of RS bytes.
 __device__ __forceinline__ uint32_t tc_lane_n(int RS, int step) {
@@ -346,15 +461,16 @@ __device__ __forceinline__ void tc_dists(const float* sp, const f32x2 (&px)[2], 
   }
 }
 
-// Calls f with the value tiles, the query chunks and the heads of a warp.
-template <typename F>
+// Calls f with the value tiles, the query chunks and the heads of a warp (one
+// where the accumulators of two would not fit the registers).
+template <int PL, typename F>
 int tc_dispatch(int nt, int dk, F&& f) {
 #define EGAT_TC(N_, HP_)                                                                                   \
   case N_:                                                                                                 \
     if (dk <= 16) return f(std::integral_constant<int, N_>{}, std::integral_constant<int, 2>{},            \
-                           std::integral_constant<int, HP_>{});                                            \
+                           std::integral_constant<int, PL == 1 ? HP_ : 1>{});                              \
     return f(std::integral_constant<int, N_>{}, std::integral_constant<int, 4>{},                          \
-             std::integral_constant<int, HP_>{})
+             std::integral_constant<int, PL == 1 ? HP_ : 1>{})
   switch (nt) {
     EGAT_TC(1, 2);
     EGAT_TC(2, 2);
@@ -363,7 +479,12 @@ int tc_dispatch(int nt, int dk, F&& f) {
     EGAT_TC(9, 2);
     EGAT_TC(16, 1);
     EGAT_TC(18, 1);
-    EGAT_TC(32, 1);
+    case 32:
+      if constexpr (PL == 1) {
+        if (dk <= 16) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+        return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+      }
+      return EGAT_ERR_UNSUPPORTED;
     default: return EGAT_ERR_UNSUPPORTED;
   }
 #undef EGAT_TC
