@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   for (int h = 0; h < HP; ++h) ref[h][0] = ref[h][1] = f2_set(__int_as_float(0x7fffffff));
 
   int buf = 0;
+  bool first = true;
   for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= L::BUFS - 1) {
     if (L::BUFS == 1)
       ld.load(sbase, k_end - k0);
@@ -102,34 +103,41 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
           }
         };
         f32x2 w[HP][4];
-        bool move = false;
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          scores(h, ref[h][0], ref[h][1], w[h]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float v[4];
-            f2_unpack(w[h][r], v[0], v[1]);
-            f2_unpack(w[h][2 + r], v[2], v[3]);
-            // all NaN without a reference
-            move |= !(fmaxf(tc_max3(v[0], v[1], v[2]), v[3]) <= 8.f);
-          }
-        }
-        auto mask = [&](int h) {   // keys past the molecule
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a, b;
-            f2_unpack(w[h][i], a, b);
-            if (j + 8 * (i >> 1) + t2 >= n) a = -INFINITY;
-            if (j + 8 * (i >> 1) + t2 + 1 >= n) b = -INFINITY;
-            w[h][i] = f2_pack(a, b);
-          }
-        };
-        if (__any_sync(~0u, move)) {
+        // once with the references and, where one has to move (the first step's always
+        // do), once without: one copy of the code
+        bool move = first;
+        first = false;
+#pragma unroll 1
+        for (;;) {
+          bool pass = false;
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
-            scores(h, 0ull, 0ull, w[h]);
-            if (j + 16 > n) mask(h);
+            scores(h, move ? 0ull : ref[h][0], move ? 0ull : ref[h][1], w[h]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float v[4];
+              f2_unpack(w[h][r], v[0], v[1]);
+              f2_unpack(w[h][2 + r], v[2], v[3]);
+              // all NaN without a reference
+              pass |= !(fmaxf(tc_max3(v[0], v[1], v[2]), v[3]) <= 8.f);
+            }
+            if (j + 16 > n)   // keys past the molecule
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float a, b;
+                f2_unpack(w[h][i], a, b);
+                if (j + 8 * (i >> 1) + t2 >= n) a = -INFINITY;
+                if (j + 8 * (i >> 1) + t2 + 1 >= n) b = -INFINITY;
+                w[h][i] = f2_pack(a, b);
+              }
+          }
+          if (move) break;
+          move = __any_sync(~0u, pass);
+          if (!move) break;
+        }
+        if (move) {
+#pragma unroll
+          for (int h = 0; h < HP; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float v[4], old, unused1;
@@ -152,10 +160,6 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
               w[h][r] = f2_add(w[h][r], shift);
               w[h][2 + r] = f2_add(w[h][2 + r], shift);
             }
-          }
-        } else if (j + 16 > n) {
-#pragma unroll
-          for (int h = 0; h < HP; ++h) mask(h);
         }
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
@@ -176,10 +180,38 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
     __syncthreads();
   }
 
+  tc_wait<0>();
+  if (kws == 1) {
+    // rows of its own: normalised in registers, through shared memory for whole chunks
+    T* rows = reinterpret_cast<T*>(tsm) + warp * 16 * L::OUTROW;   // this warp's [16][OUTROW]
+#pragma unroll
+    for (int h = 0; h < HP; ++h)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float lo, hi, mr;
+        f2_unpack(sum[h][r], lo, hi);
+        const float l = quad_sum(lo + hi), inv = l == 0.f ? 0.f : 1.f / l;
+        f2_unpack(ref[h][r], mr, hi);
+        const size_t row = r ? rowB : rowA;
+        if (t2 == 0 && p.lse && (r ? lB : lA)) p.lse[row * p.H + head0 + h] = l == 0.f ? -INFINITY : -mr * kLn2 + logf(l);
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+          tc_store2(rows + (g + 8 * r) * L::OUTROW + (x * HP + h) * 8 + t2, acc[h][x][2 * r] * inv, acc[h][x][2 * r + 1] * inv);
+      }
+    __syncwarp();
+    constexpr int PER = 16 / int(sizeof(T)), CH = HP * NT * 8 / PER;   // elements of 16 bytes, such pieces of a row
+    const int live_rows = min(16, t.rows - rw * 16);
+    for (int i = lane; i < live_rows * CH; i += 32) {
+      const int row = i / CH, e = (i % CH) * PER, c = e >> 3, x = c / HP, h = c % HP;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.m) + (size_t(t.row0) + rw * 16 + row) * (p.D * p.C) +
+                                tc_val_off(p, head0 + h, x) + (e & 7)) =
+          *reinterpret_cast<const uint4*>(rows + row * L::OUTROW + e);
+    }
+    return;
+  }
   // join the warps that shared rows, and write whole 16-byte chunks
   float* oacc = reinterpret_cast<float*>(tsm);                  // [4 warps][16][OUTROW]
   float* oml = oacc + 4 * 16 * L::OUTROW;                        // [4 warps][16][HP][2]
-  tc_wait<0>();
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < HP; ++h)

@@ -54,6 +54,7 @@ struct TcLay {
 };
 
 __device__ __forceinline__ uint32_t tc_smem(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+// 16 bytes, or (ok false) nothing from src and zeros
 __device__ __forceinline__ void tc_cp16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -153,7 +154,6 @@ struct TcPart {
   using T = typename TcStorage<PL>::T;
   static_assert(W <= 32, "a row's chunks are one warp's");
   static constexpr int ROWS = 32 / W, STEP = ROWS * (kTcThreads / 32), ITS = (kTcStage + STEP - 1) / STEP;
-  static_assert(PL == 3 || kTcStage % STEP == 0, "");
   const T* src;   // this lane's chunk of its first row
   int ld;         // elements from row to row
   uint32_t dst;
@@ -167,23 +167,25 @@ struct TcPart {
   }
   template <int RS>
   __device__ __forceinline__ void load(uint32_t st, int left, bool have) {
+    const int need = (left + 15) & ~15;   // rows that the last step of 16 meets
     if constexpr (PL == 1) {
       if (row < kTcStage) {
         if (left >= kTcStage && have) {
 #pragma unroll
-          for (int i = 0; i < ITS; ++i) tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
+          for (int i = 0; i < ITS; ++i)
+            if (kTcStage % STEP == 0 || row + i * STEP < kTcStage)
+              tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
         } else {
-#pragma unroll 1
-          for (int i = 0; i < ITS; ++i) {
-            const bool ok = have && row + i * STEP < left;
-            tc_cp16(st + dst + i * STEP * RS, ok ? src + size_t(i) * STEP * ld : src - size_t(row) * ld, ok);
-          }
+#pragma unroll
+          for (int i = 0; i < ITS; ++i)
+            if (i * STEP < need && (kTcStage % STEP == 0 || row + i * STEP < kTcStage))
+              tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, have && row + i * STEP < left);
         }
       }
     } else {
       constexpr int AT_ONCE = ITS < 4 ? ITS : 4;   // rows on their way together
 #pragma unroll 1
-      for (int i0 = 0; i0 < ITS; i0 += AT_ONCE) {
+      for (int i0 = 0; i0 * STEP < need && i0 < ITS; i0 += AT_ONCE) {
         float4 v[AT_ONCE][2];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
@@ -259,6 +261,10 @@ __device__ __forceinline__ float2 tc_float2(const __nv_bfloat16* x, bool ok) {
 __device__ __forceinline__ float2 tc_float2(const float* x, bool ok) {
   return ok ? __ldg(reinterpret_cast<const float2*>(x)) : make_float2(0.f, 0.f);
 }
+__device__ __forceinline__ void tc_store2(__nv_bfloat16* x, float a, float b) {
+  *reinterpret_cast<uint32_t*>(x) = tc_pack(a, b);
+}
+__device__ __forceinline__ void tc_store2(float* x, float a, float b) { *reinterpret_cast<float2*>(x) = make_float2(a, b); }
 // Eight elements of a row
 __device__ __forceinline__ void tc_store8(__nv_bfloat16* x, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(x) =
