@@ -595,15 +595,14 @@ __global__ void mol_reduce_kernel(MolParams p, int pos_blocks) {
     const long long j = p.a.self ? i : i - nq3;
     if (i < nq3 && p.g.dposq) {
       float s = 0.f;
-      for (int h = 0; h < p.groups; ++h) {
-        s += p.part_dq[h * nq3 + i];
-        if (p.a.self) s += p.part_dk[h * nk3 + i];
-      }
+      for (int h = 0; h < p.groups; ++h) s += p.part_dq[h * nq3 + i];
+      if (p.a.self)
+        for (int h = 0; h < p.groups_k; ++h) s += p.part_dk[h * nk3 + i];
       p.g.dposq[i] = s;
     }
     if (!p.a.self && j >= 0 && j < nk3 && p.g.dposk) {
       float s = 0.f;
-      for (int h = 0; h < p.groups; ++h) s += p.part_dk[h * nk3 + j];
+      for (int h = 0; h < p.groups_k; ++h) s += p.part_dk[h * nk3 + j];
       p.g.dposk[j] = s;
     }
     return;
@@ -692,10 +691,10 @@ int wide_log(int n, int n_mol, int rows, int groups, int enough) {
     --l;
   return l;
 }
-MolCut tile_cut(const egat_mol_shape& s, int n) {
+MolCut tile_cut(const egat_mol_shape& s, int n, bool query_gradients = false) {
   MolCut c{};
   c.tc = mol_tc_supported(s);
-  c.groups = c.tc ? s.H / mol_tc_heads(s) : s.H;
+  c.groups = c.tc ? s.H / mol_tc_heads(s, query_gradients) : s.H;
   c.splits = 1;
   if (c.tc) {
     c.rwlog = wide_log(n, s.n_mol, 16, c.groups, 2 * 148);
@@ -791,19 +790,20 @@ int backward_t(MolParams p, int k_rwlog, cudaStream_t st) {
 // Workspace of the backward pass: delta (and lse in base 2), then the partial sums of the
 // position and slope gradients.
 struct MolBwdWs {
-  MolCut cut;
+  MolCut cut, cut_k;   // query and key side
   int slots;
   size_t delta, nlse2, dq, dk, ds, total;
 };
 MolBwdWs bwd_ws(const egat_mol_shape& s) {
   MolBwdWs w;
-  w.cut = tile_cut(s, s.nq);
+  w.cut = tile_cut(s, s.nq, true);
+  w.cut_k = tile_cut(s, s.nk);
   w.slots = mol_slots(s.nq, s.n_mol, w.cut.rows);
   w.delta = 0;
   w.nlse2 = up256(sizeof(float) * size_t(s.nq) * s.H);
   w.dq = w.nlse2 + (w.cut.tc ? w.nlse2 : 0);
   w.dk = w.dq + up256(sizeof(float) * 3 * size_t(s.nq) * w.cut.groups);
-  w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * w.cut.groups);
+  w.ds = w.dk + up256(sizeof(float) * 3 * size_t(s.nk) * w.cut_k.groups);
   w.total = w.ds + up256(sizeof(float) * size_t(w.slots) * s.H);
   return w;
 }
@@ -811,15 +811,15 @@ MolBwdWs bwd_ws(const egat_mol_shape& s) {
 }  // namespace
 
 // Two heads a warp where the accumulators of two fit its registers, one of float32.
-int mol_tc_heads(const egat_mol_shape& s) {
-  return s.dtype == EGAT_BF16 && head_columns(s) <= 72 ? 2 : 1;
+int mol_tc_heads(const egat_mol_shape& s, bool query_gradients) {
+  return s.dtype == EGAT_BF16 && head_columns(s) <= (query_gradients ? 64 : 72) ? 2 : 1;
 }
 // Up to 256 value columns a head of bf16 and 144 of float32 (the accumulators of 16
 // rows and the operands beside them fill a warp's registers there), and two heads
 // where two are taken together.
 bool mol_tc_supported(const egat_mol_shape& s) {
   const int nt = head_columns(s) / 8;
-  return s.H >= mol_tc_heads(s) && (nt == 1 || nt == 2 || nt == 4 || nt == 8 || nt == 9 || nt == 16 || nt == 18 ||
+  return s.H >= mol_tc_heads(s, false) && (nt == 1 || nt == 2 || nt == 4 || nt == 8 || nt == 9 || nt == 16 || nt == 18 ||
                                     (nt == 32 && s.dtype == EGAT_BF16));
 }
 
@@ -886,9 +886,10 @@ int launch_molecule_backward(const egat_mol_shape& s, const MolArgs& a, const Mo
   p.exact_delta = s.dtype == EGAT_BF16;
   p.slots = w.slots;
   p.groups = w.cut.groups;
+  p.groups_k = w.cut_k.groups;
   p.rwlog = w.cut.rwlog;
   const bool bf16 = s.dtype == EGAT_BF16;
-  const int k_rwlog = tile_cut(s, s.nk).rwlog;
+  const int k_rwlog = w.cut_k.rwlog;
   int rc = EGAT_OK;
   if (w.cut.tc) {
     if (s.nq > 0) rc = bf16 ? mol_tc_backward_q_bf16(p, st) : mol_tc_backward_q_f32(p, st);

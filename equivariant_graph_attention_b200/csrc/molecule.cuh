@@ -18,7 +18,7 @@ struct MolParams {
   float* delta;        // [nq][H] sum_j a_ij dP_ij (minus that on the tensor-core path)
   float* nlse2;        // [nq][H] minus lse in base 2, -inf for rows without weights (tensor-core path)
   float* part_dq;      // [groups][nq][3] dL/dr of the query atoms, by group of heads
-  float* part_dk;      // [groups][nk][3] dL/dr of the key atoms
+  float* part_dk;      // [groups_k][nk][3] dL/dr of the key atoms
   float* part_ds;      // [H][slots] dL/dslope, by query tile
   void *qp, *kv;       // operand blocks of the tcgen05 kernels
   int kv_slots;        // key blocks of a head
@@ -30,7 +30,7 @@ struct MolParams {
   int slots;           // query tile slots
   int kb;              // keys per staged tile (generic kernels)
   int rwlog;           // log2 of the warps side by side over rows (tensor-core kernels)
-  int groups;          // head groups with position sums of their own
+  int groups, groups_k;   // groups of heads with position sums of their own, by side
   float scale;         // 1 / sqrt(dk)
   float cap, inv_cap;  // 0: none
   bool exact_delta;    // delta from a float32 sweep instead of G . m
@@ -116,7 +116,7 @@ __device__ __forceinline__ float mol_sqrt(float x) {
 // Tensor-core kernels in tiles of 16 << p.rwlog rows: whether they take the shape,
 // the heads that a warp takes together, and their launches.
 bool mol_tc_supported(const egat_mol_shape& s);
-int mol_tc_heads(const egat_mol_shape& s);
+int mol_tc_heads(const egat_mol_shape& s, bool query_gradients);
 int mol_tc_forward_bf16(const MolParams& p, cudaStream_t st);
 int mol_tc_forward_f32(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_q_bf16(const MolParams& p, cudaStream_t st);

@@ -12,7 +12,7 @@ namespace {
 // dP^T = H' G^T), so that the weights and dS land as the A operands of
 // dh' = a^T G and dk = dS^T Q.  A query row past the molecule has lse2 = +inf: no weight.
 template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS, bool POS>
-__global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
+__global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
   // the key rows' values as A fragments: in registers, or read again for every
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_k_tc_kernel(MolParams p) {
 
 template <int PL>
 int tc_backward_k(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch<PL>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
+  return tc_dispatch<PL, 2>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
     const size_t join = 4 * 16 * (L::OUTROW + HP * KC * 8 + 4) * 4;

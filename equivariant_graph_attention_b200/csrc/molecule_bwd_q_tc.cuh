@@ -15,7 +15,7 @@ namespace {
 // so the second sum, of weights alone, takes the rounding of m out at the end;
 // the correction is small, so nothing cancels.  A float32 m needs none of that.
 template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS, bool POS>
-__global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
+__global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3 : 4) : 2) mol_bwd_q_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
   constexpr bool FIX = PL == 1;   // m is rounded
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
   f32x2 del[HP][2] = {};
   // POS: sums over j of (slope dS', slope a) (r_j - r_i) / d and of (dS', a) d
   f32x2 gs[2][3] = {}, ga[HP][2][3] = {};
-  float sd[HP][2] = {}, sa[HP][2] = {};
+  f32x2 sd[HP][2] = {}, sa[HP][2] = {};
 
   int buf = 0;
   for (int k0 = t.o0; k0 < t.o1; k0 += kTcStage, buf ^= L::BUFS - 1) {
@@ -110,9 +110,18 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
       for (int j = kw * 16; j < n; j += kws * 16) {
         f32x2 d[2][2] = {}, ri[2][2] = {};   // distances (and their reciprocals): [8-key tile][row]
         if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
+        f32x2 u[2][2] = {}, dc[2][2] = {};   // POS: sum over the heads of slope dS; finite distances
+        if constexpr (POS) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a, b;   // a distance may be inf where the weight is zero
+            f2_unpack(d[i >> 1][i & 1], a, b);
+            dc[i >> 1][i & 1] = f2_pack(fminf(a, 3e38f), fminf(b, 3e38f));
+          }
+        }
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          float s[2][4] = {}, dp[2][4] = {};
+          float s[2][4], dp[2][4];
           tc_dot<KC, PL>(s, qf[h], st + L::QK + j * L::RK + h * KC * 16 + tc_lane_n(L::RK, 16), 0, 16, L::PK);
           const uint32_t vb = st + L::VAL + j * L::RV + h * 16;
           tc_dot<NT, PL>(dp, gf[h], vb + tc_lane_n(L::RV, HP * 16), vb + tc_lane_n2(L::RV), HP * 16, L::PV);
@@ -147,20 +156,16 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
             f32x2 ds = f2_mul(w, f2_add(dP, ndel[h][r]));
             float lo, hi;
             if (POS) {
-              const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-              const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
-              const f32x2 wr = f2_mul(w, ri[c][r]), dr = f2_mul(f2_mul(ds, slope[h]), ri[c][r]);
-#pragma unroll
-              for (int e = 0; e < 3; ++e) {
-                gs[r][e] = f2_fma(dr, dir[e], gs[r][e]);
-                if (FIX) ga[h][r][e] = f2_fma(wr, dir[e], ga[h][r][e]);
+              u[c][r] = f2_fma(ds, slope[h], u[c][r]);
+              sd[h][r] = f2_fma(ds, dc[c][r], sd[h][r]);
+              if (FIX) {
+                const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
+                const f32x2 wr = f2_mul(w, ri[c][r]);
+                ga[h][r][0] = f2_fma(wr, f2_add(at[0], px[r]), ga[h][r][0]);
+                ga[h][r][1] = f2_fma(wr, f2_add(at[kTcStage / 2], py[r]), ga[h][r][1]);
+                ga[h][r][2] = f2_fma(wr, f2_add(at[kTcStage], pz[r]), ga[h][r][2]);
+                sa[h][r] = f2_fma(w, dc[c][r], sa[h][r]);
               }
-              // d may be inf where the weight is zero
-              float d0, d1;
-              f2_unpack(d[c][r], d0, d1);
-              if (FIX) sa[h][r] += (a != 0.f ? a * d0 : 0.f) + (b != 0.f ? b * d1 : 0.f);
-              f2_unpack(ds, lo, hi);
-              sd[h][r] += (lo != 0.f ? lo * d0 : 0.f) + (hi != 0.f ? hi * d1 : 0.f);
             }
             if constexpr (CAP) {
               ds = f2_mul(ds, fx[i]);
@@ -174,6 +179,19 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
           const uint32_t kb = st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16);
           tc_apply<KC, PL>(dq[h], fd, kb, 16, L::PK);
           if constexpr (FIX) tc_apply<KC, PL>(bk[h], fa, kb, 16, L::PK);
+        }
+        if constexpr (POS) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const f32x2 f = f2_mul(u[c][r], ri[c][r]);
+              gs[r][0] = f2_fma(f, f2_add(at[0], px[r]), gs[r][0]);
+              gs[r][1] = f2_fma(f, f2_add(at[kTcStage / 2], py[r]), gs[r][1]);
+              gs[r][2] = f2_fma(f, f2_add(at[kTcStage], pz[r]), gs[r][2]);
+            }
+          }
         }
       }
     __syncthreads();
@@ -203,7 +221,10 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
       float* x = at + 2 * QN + h * PER;
       if (t2 == 0) x[0] = de, x[1] = dlt[h][r];
       if constexpr (POS) {
-        const float v0 = quad_sum(sd[h][r]), v1 = quad_sum(sa[h][r]);
+        float s0, s1, a0, a1;
+        f2_unpack(sd[h][r], s0, s1);
+        f2_unpack(sa[h][r], a0, a1);
+        const float v0 = quad_sum(s0 + s1), v1 = quad_sum(a0 + a1);
         if (t2 == 0) x[2] = v0, x[3] = v1;
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
@@ -278,9 +299,11 @@ __global__ void __launch_bounds__(kTcThreads) mol_bwd_q_tc_kernel(MolParams p) {
   }
 }
 
+// One head a warp at 72 columns: three or four blocks an SM instead of two (4,096
+// atoms capped: 0.61 -> 0.55 ms; the key side and the forward pass lose by it).
 template <int PL>
 int tc_backward_q(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch<PL>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
+  return tc_dispatch<PL, 1>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
     const size_t join = 4 * 16 * (2 * HP * KC * 8 + HP * 7 + 4) * 4;

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
 
 template <int PL>
 int tc_forward(const MolParams& p, cudaStream_t st) {
-  return tc_dispatch<PL>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
+  return tc_dispatch<PL, 2>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
     const size_t shm = std::max(L::BUFS * L::STAGE, 4 * 16 * (L::OUTROW + 2 * HP) * 4);

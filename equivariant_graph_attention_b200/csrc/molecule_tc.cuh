@@ -467,9 +467,9 @@ __device__ __forceinline__ void tc_dists(const float* sp, const f32x2 (&px)[2], 
   }
 }
 
-// Calls f with the value tiles, the query chunks and the heads of a warp (one
-// where the accumulators of two would not fit the registers).
-template <int PL, typename F>
+// Calls f with the value tiles, the query chunks and the heads of a warp: two for up
+// to 64 value columns, HP9 for 72, and one where the registers would not hold two.
+template <int PL, int HP9, typename F>
 int tc_dispatch(int nt, int dk, F&& f) {
 #define EGAT_TC(N_, HP_)                                                                                   \
   case N_:                                                                                                 \
@@ -482,7 +482,7 @@ int tc_dispatch(int nt, int dk, F&& f) {
     EGAT_TC(2, 2);
     EGAT_TC(4, 2);
     EGAT_TC(8, 2);
-    EGAT_TC(9, 2);
+    EGAT_TC(9, HP9);
     EGAT_TC(16, 1);
     EGAT_TC(18, 1);
     case 32:
