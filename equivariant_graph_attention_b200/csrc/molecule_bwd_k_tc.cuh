@@ -45,6 +45,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
       }
     }
   };
+  // its own rows of k and h' pass through the stage that the queries take last
+  const uint32_t own = sbase + (L::BUFS - 1) * L::STAGE, own_rows = rw * 16;
+  {
+    TcLoader<NT, KC, HP, PL> rows;
+    rows.init(p, p.a.k, p.a.hp, nullptr, head0, t.row0);
+    rows.pos = nullptr;
+    rows.load(own, t.rows);
+  }
+  tc_commit();
   if (t.o0 < t.o1) {
     ld.init(p, p.a.q, p.g.g, p.a.posq, head0, t.o0);
     if (L::BUFS == 2) load(t.o0, 0);
@@ -53,10 +62,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
 
   uint32_t kf[HP][PL][KC][2], vf[HP][PL][VREG ? NT : 1][2];
   f32x2 slope[HP] = {}, px[2] = {}, py[2] = {}, pz[2] = {};
+  tc_wait<1>();
+  __syncthreads();
 #pragma unroll
   for (int h = 0; h < HP; ++h) {
-    tc_frag_qk<KC, PL>(p, p.a.k, rowA, rowB, lA, lB, head0 + h, kf[h]);
-    if constexpr (VREG) tc_frag_val<NT, PL>(p, p.a.hp, rowA, rowB, lA, lB, head0 + h, vf[h]);
+    tc_frag_rows<KC, PL>(own + L::QK + own_rows * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK, kf[h]);
+    if constexpr (VREG)
+      tc_frag_rows<NT, PL>(own + L::VAL + own_rows * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV, vf[h]);
     if constexpr (BIAS) slope[h] = f2_set(-p.a.slope[head0 + h] * kLog2e);
   }
   if constexpr (BIAS)
@@ -72,6 +84,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
 
   float dk[HP][KC][4] = {}, dv[HP][NT][4] = {};
   f32x2 gs[2][3] = {};
+  __syncthreads();   // the loop fills that stage
   int buf = 0;
   for (int q0 = t.o0; q0 < t.o1; q0 += kTcStage, buf ^= L::BUFS - 1) {
     if (L::BUFS == 1)
@@ -155,63 +168,62 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
     __syncthreads();
   }
 
-  // join the warps that shared rows: dh' first, then dk and the positions
-  constexpr int QN = HP * KC * 8, ROW = QN + (POS ? 3 : 0) + 1;
-  float* oacc = reinterpret_cast<float*>(tsm);            // [4 warps][16][OUTROW]
-  float* o = oacc + 4 * 16 * L::OUTROW;                    // [4 warps][16][ROW]
   tc_wait<0>();
   __syncthreads();
+  float gs2[2][3];
+  if (POS)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        float lo, hi;
+        f2_unpack(gs[r][e], lo, hi);
+        gs2[r][e] = quad_sum(lo + hi);
+      }
+  if (kws > 1)
+    tc_join<HP * (NT + KC) * 4 + (POS ? 6 : 0)>(reinterpret_cast<float*>(tsm), rw, 1 << p.rwlog, kw, kws, [&](auto&& f) {
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f(dv[h][x][e]);
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f(dk[h][c][e]);
+      }
+      if constexpr (POS)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 3; ++e) f(gs2[r][e]);
+    });
+  if (kw != 0 || !warp_live) return;
+  constexpr int OUT = HP * KC * 8 + 8;
+  T* rows = reinterpret_cast<T*>(tsm) + rw * 16 * (L::OUTROW + OUT);   // [16][OUTROW] values, [16][OUT] keys
+  T* krows = rows + 16 * L::OUTROW;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const int row = warp * 16 + g + 8 * r;
 #pragma unroll
     for (int h = 0; h < HP; ++h) {
 #pragma unroll
       for (int x = 0; x < NT; ++x)
-        *reinterpret_cast<float2*>(oacc + row * L::OUTROW + (x * HP + h) * 8 + t2) =
-            make_float2(dv[h][x][2 * r], dv[h][x][2 * r + 1]);
+        tc_store2(rows + (g + 8 * r) * L::OUTROW + (x * HP + h) * 8 + t2, dv[h][x][2 * r], dv[h][x][2 * r + 1]);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) o[row * ROW + (h * KC + c) * 8 + t2 + e] = dk[h][c][2 * r + e];
+        tc_store2(krows + (g + 8 * r) * OUT + (h * KC + c) * 8 + t2, p.scale * dk[h][c][2 * r], p.scale * dk[h][c][2 * r + 1]);
     }
-    if constexpr (POS)
+    if (POS && t2 == 0 && (r ? lB : lA)) {
+      float* at = p.part_dk + (size_t(blockIdx.y) * p.nk + (r ? rowB : rowA)) * 3;
 #pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        float g0, g1;
-        f2_unpack(gs[r][e], g0, g1);
-        const float x = quad_sum(g0 + g1);
-        if (t2 == 0) o[row * ROW + QN + e] = x;
-      }
-  }
-  __syncthreads();
-  const int rws = 1 << p.rwlog, kc = p.dk >> 3;
-  for (int i = threadIdx.x; i < t.rows * HP * NT; i += kTcThreads) {
-    const int row = i / (HP * NT), c = i % (HP * NT), x = c / HP, h = c % HP;
-    float s[8] = {};
-    for (int w = 0; w < kws; ++w)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += oacc[(w * rws * 16 + row) * L::OUTROW + c * 8 + e];
-    tc_store8(static_cast<T*>(p.g.dhp) + (size_t(t.row0) + row) * (p.D * p.C) + tc_val_off(p, head0 + h, x), s);
-  }
-  auto sum_at = [&](int row, int i) {
-    float x = 0.f;
-    for (int w = 0; w < kws; ++w) x += o[(w * rws * 16 + row) * ROW + i];
-    return x;
-  };
-  for (int i = threadIdx.x; i < t.rows * HP * KC; i += kTcThreads) {
-    const int row = i / (HP * KC), c = i % (HP * KC), h = c / KC, cc = c % KC;
-    if (cc >= kc) continue;
-    float u[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = p.scale * sum_at(row, c * 8 + e);
-    tc_store8(static_cast<T*>(p.g.dk) + ((size_t(t.row0) + row) * p.H + head0 + h) * p.dk + cc * 8, u);
-  }
-  if constexpr (POS)
-    for (int i = threadIdx.x; i < t.rows * 3; i += kTcThreads) {
-      const int row = i / 3, e = i % 3;
-      p.part_dk[(size_t(blockIdx.y) * p.nk + t.row0 + row) * 3 + e] = -kLn2 * sum_at(row, QN + e);
+      for (int e = 0; e < 3; ++e) at[e] = -kLn2 * gs2[r][e];
     }
+  }
+  __syncwarp();
+  const int live = min(16, t.rows - rw * 16);
+  tc_write_vals<NT, HP, L::OUTROW>(p, rows, p.g.dhp, head0, size_t(t.row0) + rw * 16, live);
+  tc_write_qk<KC, HP, OUT>(p, krows, p.g.dk, head0, size_t(t.row0) + rw * 16, live);
 }
 
 template <int PL>
@@ -219,8 +231,8 @@ int tc_backward_k(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 2>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
-    const size_t join = 4 * 16 * (L::OUTROW + HP * KC * 8 + 4) * 4;
-    const size_t shm = std::max(size_t(L::BUFS * L::STAGE), join);
+    const int shm = std::max({L::BUFS * L::STAGE, tc_join_bytes(HP * (NT + KC) * 4 + 6),
+                              int(64 * (L::OUTROW + HP * KC * 8 + 8) * sizeof(typename L::T))});
     const dim3 grid(mol_slots(p.nk, p.nmol, 16 << p.rwlog), p.H / HP);
     // positions come with a bias
     if (p.want_pos)

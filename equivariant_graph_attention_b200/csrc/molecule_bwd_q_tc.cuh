@@ -7,6 +7,11 @@
 namespace egat {
 namespace {
 
+// sums of a thread that the warps of a row join
+constexpr int q_sums(int kc, int hp, bool fix, bool pos) {
+  return hp * (kc * 4 * (fix ? 2 : 1) + 2 * ((fix ? 1 : 0) + (pos ? (fix ? 5 : 1) : 0))) + (pos ? 6 : 0);
+}
+
 // dL/dq, the row sums delta_i = sum_j a_ij dP_ij and, with POS, the query side
 // of dL/dr and dL/dslope, in one sweep over the keys.  The sweep takes
 // dS' = a (dP - delta') with delta' = G . m from the stored, rounded m, and sums
@@ -19,6 +24,7 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
   constexpr bool FIX = PL == 1;   // m is rounded
+  constexpr int SUMS = q_sums(KC, HP, FIX, POS), OUT = HP * KC * 8 + 8;
   extern __shared__ __align__(128) unsigned char tsm[];
   const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -32,6 +38,15 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
   const bool warp_live = rw * 16 < t.rows, lA = rA < t.rows, lB = rB < t.rows;
   const size_t rowA = size_t(t.row0) + rA, rowB = rowA + 8;
   const uint32_t sbase = tc_smem(tsm);
+  // its own rows of q and G, then of m, pass through the stage that the keys take last
+  const uint32_t own = sbase + (L::BUFS - 1) * L::STAGE, own_rows = rw * 16;
+  {
+    TcLoader<NT, KC, HP, PL> rows;
+    rows.init(p, p.a.q, p.g.g, nullptr, head0, t.row0);
+    rows.pos = nullptr;
+    rows.load(own, t.rows);
+  }
+  tc_commit();
   TcLoader<NT, KC, HP, PL> ld;
   if (t.o0 < t.o1) {
     ld.init(p, p.a.k, p.a.hp, p.a.posk, head0, t.o0);
@@ -42,22 +57,38 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
   uint32_t qf[HP][PL][KC][2], gf[HP][PL][NT][2];
   float lse2[HP][2], dlt[HP][2];   // rows that are not there: lse2 = +inf, no weight
   f32x2 slope[HP] = {}, px[2] = {}, py[2] = {}, pz[2] = {};
+  tc_wait<1>();
+  __syncthreads();
 #pragma unroll
   for (int h = 0; h < HP; ++h) {
-    tc_frag_qk<KC, PL>(p, p.a.q, rowA, rowB, lA, lB, head0 + h, qf[h]);
-    tc_frag_val<NT, PL>(p, p.g.g, rowA, rowB, lA, lB, head0 + h, gf[h]);
-    float d0 = 0.f, d1 = 0.f;
+    tc_frag_rows<KC, PL>(own + L::QK + own_rows * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK, qf[h]);
+    tc_frag_rows<NT, PL>(own + L::VAL + own_rows * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV, gf[h]);
+  }
+  __syncthreads();
+  {
+    TcPart<HP * NT, PL> rows;
+    const int c = lane % (HP * NT);
+    rows.init(static_cast<const T*>(p.g.m), p.D * p.C, tc_val_off(p, head0 + c % HP, c / HP), t.row0, L::VAL, L::RV);
+    rows.template load<L::RV>(own, t.rows, true);
+  }
+  tc_commit();
+  tc_wait<0>();
+  __syncthreads();
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int o = tc_val_off(p, head0 + h, c) + t2;
+  for (int h = 0; h < HP; ++h) {
+    float d0 = 0.f, d1 = 0.f;
+    uint32_t mf[PL][NT][2];
+    tc_frag_rows<NT, PL>(own + L::VAL + own_rows * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV, mf);
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const size_t at = (r ? rowB : rowA) * (p.D * p.C) + o;
-        const float2 m = tc_float2(static_cast<const T*>(p.g.m) + at, r ? lB : lA);
-        const float2 x = tc_float2(static_cast<const T*>(p.g.g) + at, r ? lB : lA);
+        uint32_t mw[PL], gw[PL];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) mw[k] = mf[k][c][r], gw[k] = gf[h][k][c][r];
+        const float2 m = tc_value<PL>(mw), x = tc_value<PL>(gw);
         (r ? d1 : d0) += fmaf(m.x, x.x, m.y * x.y);
       }
-    }
     dlt[h][0] = quad_sum(d0);
     dlt[h][1] = quad_sum(d1);
 #pragma unroll
@@ -93,6 +124,7 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
   f32x2 gs[2][3] = {}, ga[HP][2][3] = {};
   f32x2 sd[HP][2] = {}, sa[HP][2] = {};
 
+  __syncthreads();   // the loop fills that stage
   int buf = 0;
   for (int k0 = t.o0; k0 < t.o1; k0 += kTcStage, buf ^= L::BUFS - 1) {
     if (L::BUFS == 1)
@@ -197,104 +229,123 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
     __syncthreads();
   }
 
-  // Join the warps that shared rows.  A row's floats: dq, sum a f' k (8 KC HP
-  // each), then per head delta, delta' and, with POS, the sums above.
-  constexpr int QN = HP * KC * 8, PER = POS ? 7 : 2, ROW = 2 * QN + HP * PER + (POS ? 3 : 0) + 1;
-  float* o = reinterpret_cast<float*>(tsm);   // [4 warps][16][ROW]
   tc_wait<0>();
   __syncthreads();
+  // sums of a row: its four lanes', then those of the warps that shared it
+  float del2[HP][2], sd2[HP][2], sa2[HP][2], ga2[HP][2][3], gs2[2][3];
+  auto both = [](f32x2 v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return quad_sum(lo + hi);
+  };
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    float* at = o + (warp * 16 + g + 8 * r) * ROW;
 #pragma unroll
     for (int h = 0; h < HP; ++h) {
+      if (FIX) del2[h][r] = both(del[h][r]);
+      if (POS) {
+        sd2[h][r] = both(sd[h][r]);
+        if (FIX) {
+          sa2[h][r] = both(sa[h][r]);
 #pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          at[(h * KC + c) * 8 + t2 + e] = dq[h][c][2 * r + e];
-          if (FIX) at[QN + (h * KC + c) * 8 + t2 + e] = bk[h][c][2 * r + e];
-        }
-      float lo, hi;
-      f2_unpack(del[h][r], lo, hi);
-      const float de = quad_sum(lo + hi);
-      float* x = at + 2 * QN + h * PER;
-      if (t2 == 0) x[0] = de, x[1] = dlt[h][r];
-      if constexpr (POS) {
-        float s0, s1, a0, a1;
-        f2_unpack(sd[h][r], s0, s1);
-        f2_unpack(sa[h][r], a0, a1);
-        const float v0 = quad_sum(s0 + s1), v1 = quad_sum(a0 + a1);
-        if (t2 == 0) x[2] = v0, x[3] = v1;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          float g0, g1;
-          f2_unpack(ga[h][r][e], g0, g1);
-          const float v2 = quad_sum(g0 + g1);
-          if (t2 == 0) x[4 + e] = v2;
+          for (int e = 0; e < 3; ++e) ga2[h][r][e] = both(ga[h][r][e]);
         }
       }
     }
-    if constexpr (POS)
+    if (POS)
 #pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        float g0, g1;
-        f2_unpack(gs[r][e], g0, g1);
-        const float v3 = quad_sum(g0 + g1);
-        if (t2 == 0) at[2 * QN + HP * PER + e] = v3;
+      for (int e = 0; e < 3; ++e) gs2[r][e] = both(gs[r][e]);
+  }
+  const int rws = 1 << p.rwlog;
+  if (kws > 1)
+    tc_join<SUMS>(reinterpret_cast<float*>(tsm), rw, rws, kw, kws, [&](auto&& f) {
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f(dq[h][c][e]);
+            if constexpr (FIX) f(bk[h][c][e]);
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if constexpr (FIX) f(del2[h][r]);
+          if constexpr (POS) {
+            f(sd2[h][r]);
+            if constexpr (FIX) {
+              f(sa2[h][r]);
+#pragma unroll
+              for (int e = 0; e < 3; ++e) f(ga2[h][r][e]);
+            }
+          }
+        }
       }
-  }
-  __syncthreads();
-  const int rws = 1 << p.rwlog, kc = p.dk >> 3;
-  auto sum_at = [&](int row, int i) {
-    float x = 0.f;
-    for (int w = 0; w < kws; ++w) x += o[(w * rws * 16 + row) * ROW + i];
-    return x;
-  };
-  for (int i = threadIdx.x; i < t.rows * HP * KC; i += kTcThreads) {
-    const int row = i / (HP * KC), c = i % (HP * KC), h = c / KC, cc = c % KC;
-    if (cc >= kc) continue;
-    const int x = 2 * QN + h * PER;
-    const float eps = FIX ? o[row * ROW + x + 1] - sum_at(row, x) : 0.f;
-    float u[8];
+      if constexpr (POS)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      u[e] = sum_at(row, c * 8 + e);
-      if (FIX) u[e] = fmaf(eps, sum_at(row, QN + c * 8 + e), u[e]);
-      u[e] *= p.scale;
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 3; ++e) f(gs2[r][e]);
+    });
+  __shared__ float warp_ds[4][HP];
+  if (kw == 0 && warp_live) {
+    T* rows = reinterpret_cast<T*>(tsm) + rw * 16 * OUT;
+    float ds_sum[HP] = {};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool ok = r ? lB : lA;
+      const size_t row = r ? rowB : rowA;
+      float pos[3];
+      if (POS)
+#pragma unroll
+        for (int e = 0; e < 3; ++e) pos[e] = -kLn2 * gs2[r][e];   // slope was -slope log2 e there
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        const float eps = FIX ? dlt[h][r] - del2[h][r] : 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          float x = dq[h][c][2 * r], y = dq[h][c][2 * r + 1];
+          if constexpr (FIX) {
+            x = fmaf(eps, bk[h][c][2 * r], x);
+            y = fmaf(eps, bk[h][c][2 * r + 1], y);
+          }
+          tc_store2(rows + (g + 8 * r) * OUT + (h * KC + c) * 8 + t2, p.scale * x, p.scale * y);
+        }
+        if (t2 == 0 && ok) {
+          p.delta[row * p.H + head0 + h] = eps - dlt[h][r];
+          p.nlse2[row * p.H + head0 + h] = lse2[h][r] == INFINITY ? -INFINITY : -lse2[h][r];
+        }
+        if (POS) {
+          // directions point from i to j: dL/dr_i = sum slope dS (r_j - r_i) / d
+          if (FIX)
+#pragma unroll
+            for (int e = 0; e < 3; ++e) pos[e] = fmaf(p.a.slope[head0 + h] * eps, ga2[h][r][e], pos[e]);
+          if (t2 == 0 && ok) ds_sum[h] -= FIX ? fmaf(eps, sa2[h][r], sd2[h][r]) : sd2[h][r];
+        }
+      }
+      if (POS && t2 == 0 && ok) {
+        float* at = p.part_dq + (size_t(blockIdx.y) * p.nq + row) * 3;
+        at[0] = pos[0], at[1] = pos[1], at[2] = pos[2];
+      }
     }
-    tc_store8(static_cast<T*>(p.g.dq) + ((size_t(t.row0) + row) * p.H + head0 + h) * p.dk + cc * 8, u);
-  }
-  for (int i = threadIdx.x; i < t.rows * HP; i += kTcThreads) {
-    const int row = i / HP, h = i % HP;
-    const size_t at = (size_t(t.row0) + row) * p.H + head0 + h;
-    const float x = p.g.lse[at] * kLog2e;
-    p.delta[at] = FIX ? -sum_at(row, 2 * QN + h * PER) : -o[row * ROW + 2 * QN + h * PER + 1];
-    p.nlse2[at] = x == -INFINITY ? -INFINITY : -x;   // a row without weights stays without
+    __syncwarp();
+    tc_write_qk<KC, HP, OUT>(p, rows, p.g.dq, head0, size_t(t.row0) + rw * 16, min(16, t.rows - rw * 16));
+    if (POS) {
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        float x = ds_sum[h];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+        if (lane == 0) warp_ds[rw][h] = x;
+      }
+    }
   }
   if constexpr (POS) {
-    // positions: slope here is -slope log2 e, and the directions point from i to j:
-    //   dL/dr_i = sum slope dS (r_j - r_i) / d
-    for (int i = threadIdx.x; i < t.rows * 3; i += kTcThreads) {
-      const int row = i / 3, e = i % 3;
-      float x = -kLn2 * sum_at(row, 2 * QN + HP * PER + e);
-#pragma unroll
-      for (int h = 0; h < (FIX ? HP : 0); ++h) {
-        const int at = 2 * QN + h * PER;
-        x = fmaf(p.a.slope[head0 + h] * (o[row * ROW + at + 1] - sum_at(row, at)), sum_at(row, at + 4 + e), x);
-      }
-      p.part_dq[(size_t(blockIdx.y) * p.nq + t.row0 + row) * 3 + e] = x;
-    }
-    if (warp < HP) {
+    __syncthreads();
+    if (threadIdx.x < HP) {
       float x = 0.f;
-      for (int row = lane; row < t.rows; row += 32) {
-        const int at = 2 * QN + warp * PER;
-        x -= sum_at(row, at + 2);
-        if (FIX) x -= (o[row * ROW + at + 1] - sum_at(row, at)) * sum_at(row, at + 3);
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(~0u, x, s);
-      if (lane == 0) p.part_ds[size_t(head0 + warp) * p.slots + blockIdx.x] = x;
+      for (int w = 0; w < rws && w * 16 < t.rows; ++w) x += warp_ds[w][threadIdx.x];
+      p.part_ds[size_t(head0 + threadIdx.x) * p.slots + blockIdx.x] = x;
     }
   }
 }
@@ -306,8 +357,8 @@ int tc_backward_q(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 1>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
-    const size_t join = 4 * 16 * (2 * HP * KC * 8 + HP * 7 + 4) * 4;
-    const size_t shm = std::max(size_t(L::BUFS * L::STAGE), join);
+    const int shm = std::max({L::BUFS * L::STAGE, tc_join_bytes(q_sums(KC, HP, PL == 1, true)),
+                              int(64 * (HP * KC * 8 + 8) * sizeof(typename L::T))});
     const dim3 grid(p.slots, p.H / HP);
     // positions come with a bias
     if (p.want_pos)

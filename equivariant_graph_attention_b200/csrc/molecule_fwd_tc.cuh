@@ -199,14 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
           tc_store2(rows + (g + 8 * r) * L::OUTROW + (x * HP + h) * 8 + t2, acc[h][x][2 * r] * inv, acc[h][x][2 * r + 1] * inv);
       }
     __syncwarp();
-    constexpr int PER = 16 / int(sizeof(T)), CH = HP * NT * 8 / PER;   // elements of 16 bytes, such pieces of a row
-    const int live_rows = min(16, t.rows - rw * 16);
-    for (int i = lane; i < live_rows * CH; i += 32) {
-      const int row = i / CH, e = (i % CH) * PER, c = e >> 3, x = c / HP, h = c % HP;
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.m) + (size_t(t.row0) + rw * 16 + row) * (p.D * p.C) +
-                                tc_val_off(p, head0 + h, x) + (e & 7)) =
-          *reinterpret_cast<const uint4*>(rows + row * L::OUTROW + e);
-    }
+    tc_write_vals<NT, HP, L::OUTROW>(p, rows, p.m, head0, size_t(t.row0) + rw * 16, min(16, t.rows - rw * 16));
     return;
   }
   // join the warps that shared rows, and write whole 16-byte chunks

@@ -24,6 +24,8 @@
 // asynchronously, and a warp takes one head.
 #pragma once
 
+#include <algorithm>
+
 #include "molecule.cuh"
 
 namespace egat {
@@ -305,6 +307,80 @@ __device__ __forceinline__ void tc_frag_val(const MolParams& p, const void* src,
 #pragma unroll
       for (int k = 0; k < PL; ++k) f[k][c][r] = w[k];
     }
+}
+
+// ... and from shared memory: base is the lane's address of chunk 0 of its rows (row
+// by lane & 15, chunk by lane / 16)
+template <int NC, int PL>
+__device__ __forceinline__ void tc_frag_rows(uint32_t base, int step, int plane, uint32_t (&f)[PL][NC][2]) {
+#pragma unroll
+  for (int k = 0; k < PL; ++k) {
+#pragma unroll
+    for (int c = 0; c + 1 < NC; c += 2) {
+      uint32_t b[4];
+      tc_ldsm4(base + k * plane + c * step, b);
+      f[k][c][0] = b[0], f[k][c][1] = b[1], f[k][c + 1][0] = b[2], f[k][c + 1][1] = b[3];
+    }
+    if constexpr (NC & 1) tc_ldsm2(base + k * plane + (NC - 1) * step, f[k][NC - 1][0], f[k][NC - 1][1]);
+  }
+}
+// the numbers of a pair, from its planes
+template <int PL>
+__device__ __forceinline__ float2 tc_value(const uint32_t (&w)[PL]) {
+  float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = PL - 1; k >= 0; --k) {
+    v.x += __uint_as_float(w[k] << 16);
+    v.y += __uint_as_float(w[k] & 0xffff0000u);
+  }
+  return v;
+}
+
+// Sums of the warps that share rows: visit(f) calls f on a thread's N sums; the
+// first of the warps ends with the total.  The other threads only take part.
+template <int N, typename V>
+__device__ __forceinline__ void tc_join(float* sm, int rw, int rws, int kw, int kws, V&& visit) {
+  const int lane = threadIdx.x & 31;
+  if (kw > 0) {
+    float* o = sm + size_t((kw - 1) * rws + rw) * N * 32 + lane;
+    visit([&](float& x) {
+      *o = x;
+      o += 32;
+    });
+  }
+  __syncthreads();
+  if (kw == 0)
+    for (int w = 1; w < kws; ++w) {
+      const float* o = sm + size_t((w - 1) * rws + rw) * N * 32 + lane;
+      visit([&](float& x) {
+        x += *o;
+        o += 32;
+      });
+    }
+  __syncthreads();
+}
+constexpr int tc_join_bytes(int n) { return 3 * n * 32 * 4; }   // at most three warps' sums
+
+// A warp's 16 rows of values, or of queries or keys, from shared memory (rows of
+// OUT elements) to global memory in 16-byte pieces.
+template <int NT, int HP, int OUT, typename T>
+__device__ __forceinline__ void tc_write_vals(const MolParams& p, const T* rows, void* out, int head0, size_t row0, int live) {
+  constexpr int PER = 16 / int(sizeof(T)), CH = HP * NT * 8 / PER;   // elements of a piece, pieces of a row
+  for (int i = threadIdx.x & 31; i < live * CH; i += 32) {
+    const int row = i / CH, e = (i % CH) * PER, c = e >> 3, x = c / HP, h = c % HP;
+    *reinterpret_cast<uint4*>(static_cast<T*>(out) + (row0 + row) * (p.D * p.C) + tc_val_off(p, head0 + h, x) + (e & 7)) =
+        *reinterpret_cast<const uint4*>(rows + row * OUT + e);
+  }
+}
+template <int KC, int HP, int OUT, typename T>
+__device__ __forceinline__ void tc_write_qk(const MolParams& p, const T* rows, void* out, int head0, size_t row0, int live) {
+  constexpr int PER = 16 / int(sizeof(T)), CH = HP * KC * 8 / PER;
+  for (int i = threadIdx.x & 31; i < live * CH; i += 32) {
+    const int row = i / CH, e = (i % CH) * PER, h = e / (KC * 8), d = e % (KC * 8);
+    if (d < p.dk)
+      *reinterpret_cast<uint4*>(static_cast<T*>(out) + ((row0 + row) * p.H + head0 + h) * p.dk + d) =
+          *reinterpret_cast<const uint4*>(rows + row * OUT + e);
+  }
 }
 
 // acc (16 rows x 16 other rows) = (or, with ADD, +=) A (16 rows x NC chunks) . (other rows)^T:
