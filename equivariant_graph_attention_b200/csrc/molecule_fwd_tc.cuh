@@ -31,6 +31,16 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   const int k_begin = t.o0 + int(blockIdx.z) * per * kTcStage;
   const int k_end = min(t.o1, k_begin + per * kTcStage);
   const uint32_t sbase = tc_smem(tsm);
+  // its own query rows pass through the stage that the keys take last
+  const uint32_t own = sbase + (L::BUFS - 1) * L::STAGE;
+  {
+    TcPart<HP * KC, PL> rows;
+    const int c = lane % (HP * KC);
+    const bool have = (c % KC) * 8 < p.dk;
+    rows.init(static_cast<const T*>(p.a.q), p.H * p.dk, (head0 + c / KC) * p.dk + (have ? c % KC : 0) * 8, t.row0, L::QK, L::RK);
+    rows.template load<L::RK>(own, t.rows, have);
+  }
+  tc_commit();
   TcLoader<NT, KC, HP, PL> ld;
   if (k_begin < k_end) {
     ld.init(p, p.a.k, p.a.hp, p.a.posk, head0, k_begin);
@@ -39,8 +49,11 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   tc_commit();
 
   uint32_t qf[HP][PL][KC][2];
+  tc_wait<1>();
+  __syncthreads();
 #pragma unroll
-  for (int h = 0; h < HP; ++h) tc_frag_qk<KC, PL>(p, p.a.q, rowA, rowB, lA, lB, head0 + h, qf[h]);
+  for (int h = 0; h < HP; ++h)
+    tc_frag_rows<KC, PL>(own + L::QK + rw * 16 * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK, qf[h]);
   f32x2 px[2] = {}, py[2] = {}, pz[2] = {}, slope[HP] = {};   // minus the rows' positions
   if constexpr (BIAS) {
 #pragma unroll
@@ -63,6 +76,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
 #pragma unroll
   for (int h = 0; h < HP; ++h) ref[h][0] = ref[h][1] = f2_set(__int_as_float(0x7fffffff));
 
+  __syncthreads();   // the loop fills that stage
   int buf = 0;
   bool first = true;
   for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= L::BUFS - 1) {
@@ -106,7 +120,6 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
         // once with the references and, where one has to move (the first step's always
         // do), once without: one copy of the code
         bool move = first;
-        first = false;
 #pragma unroll 1
         for (;;) {
           bool pass = false;
@@ -151,16 +164,18 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
               const float f = none || isnan(old) ? 0.f : fast_exp2(-old - up);
               ref[h][r] = f2_set(none ? __int_as_float(0x7fffffff) : -up);
               sum[h][r] = f2_mul(sum[h][r], f2_set(f));
+              if (!first)
 #pragma unroll
-              for (int x = 0; x < NT; ++x) {
-                acc[h][x][2 * r] *= f;
-                acc[h][x][2 * r + 1] *= f;
-              }
+                for (int x = 0; x < NT; ++x) {
+                  acc[h][x][2 * r] *= f;
+                  acc[h][x][2 * r + 1] *= f;
+                }
               const f32x2 shift = f2_set(none ? 0.f : -up);
               w[h][r] = f2_add(w[h][r], shift);
               w[h][2 + r] = f2_add(w[h][2 + r], shift);
             }
         }
+        first = false;
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
           uint32_t pf[PL][2][2];

@@ -362,25 +362,38 @@ __device__ __forceinline__ void tc_join(float* sm, int rw, int rws, int kw, int 
 constexpr int tc_join_bytes(int n) { return 3 * n * 32 * 4; }   // at most three warps' sums
 
 // A warp's 16 rows of values, or of queries or keys, from shared memory (rows of
-// OUT elements) to global memory in 16-byte pieces.
+// OUT elements) to global memory in 16-byte pieces: a lane keeps its piece and
+// advances by whole rows.
+template <int CH, int OUT, typename T, typename F>
+__device__ __forceinline__ void tc_write_rows(const T* rows, T* out, size_t ld, int live, F&& offset) {
+  constexpr int PER = 16 / int(sizeof(T)), ROWS = CH <= 32 ? 32 / CH : 1;
+  const int lane = threadIdx.x & 31;
+  for (int piece = CH <= 32 ? lane % CH : lane; piece < CH; piece += 32) {
+    const int off = offset(piece * PER);
+    if (off < 0) continue;
+    int row = CH <= 32 ? lane / CH : 0;
+    if (row >= ROWS) continue;
+    const T* from = rows + row * OUT + piece * PER;
+    T* to = out + row * ld + off;
+    for (; row < live; row += ROWS, from += ROWS * OUT, to += ROWS * ld)
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+  }
+}
 template <int NT, int HP, int OUT, typename T>
 __device__ __forceinline__ void tc_write_vals(const MolParams& p, const T* rows, void* out, int head0, size_t row0, int live) {
-  constexpr int PER = 16 / int(sizeof(T)), CH = HP * NT * 8 / PER;   // elements of a piece, pieces of a row
-  for (int i = threadIdx.x & 31; i < live * CH; i += 32) {
-    const int row = i / CH, e = (i % CH) * PER, c = e >> 3, x = c / HP, h = c % HP;
-    *reinterpret_cast<uint4*>(static_cast<T*>(out) + (row0 + row) * (p.D * p.C) + tc_val_off(p, head0 + h, x) + (e & 7)) =
-        *reinterpret_cast<const uint4*>(rows + row * OUT + e);
-  }
+  const size_t ld = p.D * p.C;
+  tc_write_rows<HP * NT * 8 * int(sizeof(T)) / 16, OUT>(rows, static_cast<T*>(out) + row0 * ld, ld, live, [&](int e) {
+    const int c = e >> 3;
+    return tc_val_off(p, head0 + c % HP, c / HP) + (e & 7);
+  });
 }
 template <int KC, int HP, int OUT, typename T>
 __device__ __forceinline__ void tc_write_qk(const MolParams& p, const T* rows, void* out, int head0, size_t row0, int live) {
-  constexpr int PER = 16 / int(sizeof(T)), CH = HP * KC * 8 / PER;
-  for (int i = threadIdx.x & 31; i < live * CH; i += 32) {
-    const int row = i / CH, e = (i % CH) * PER, h = e / (KC * 8), d = e % (KC * 8);
-    if (d < p.dk)
-      *reinterpret_cast<uint4*>(static_cast<T*>(out) + ((row0 + row) * p.H + head0 + h) * p.dk + d) =
-          *reinterpret_cast<const uint4*>(rows + row * OUT + e);
-  }
+  const size_t ld = p.H * p.dk;
+  tc_write_rows<HP * KC * 8 * int(sizeof(T)) / 16, OUT>(rows, static_cast<T*>(out) + row0 * ld, ld, live, [&](int e) {
+    const int h = e / (KC * 8), d = e % (KC * 8);
+    return d < p.dk ? (head0 + h) * p.dk + d : -1;
+  });
 }
 
 // acc (16 rows x 16 other rows) = (or, with ADD, +=) A (16 rows x NC chunks) . (other rows)^T:
