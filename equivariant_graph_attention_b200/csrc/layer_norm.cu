@@ -135,6 +135,10 @@ __device__ __forceinline__ void load_f32(const float* p, int c, float dflt, floa
 template <int E, int V>
 constexpr bool norm_hold() { return E == 8 && V <= 4; }
 
+// The warps' column sums lie side by side in shared memory up to 512 columns.
+template <int E, int V>
+constexpr bool norm_side() { return E == 8 && V <= 2; }
+
 template <typename T, int E, int TPR, int V>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(NormParams p) {
   constexpr int NT = norm_threads<TPR>();
@@ -230,7 +234,7 @@ template <typename T, int E, int TPR, int V>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParams p) {
   constexpr int NT = norm_threads<TPR>(), WARPS = NT / 32;
   constexpr bool HOLD = norm_hold<E, V>();
-  extern __shared__ float sums[];   // [2][width]
+  extern __shared__ float sums[];   // [2][width], by warp where norm_side
   __shared__ float red[32];
   const int lane = threadIdx.x % TPR;
   float dw[V][E] = {}, db[V][E] = {}, hw[HOLD ? V : 1][E];
@@ -329,6 +333,29 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
           dw[i][e] += __shfl_xor_sync(~0u, dw[i][e], o);
           db[i][e] += __shfl_xor_sync(~0u, db[i][e], o);
         }
+    if constexpr (norm_side<E, V>()) {
+      if (int(threadIdx.x % 32) < TPR) {
+        float* own = sums + (threadIdx.x / 32) * 2 * p.width;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int c = (lane + i * TPR) * E;
+          if (c < p.width)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              own[c + e] = dw[i][e];
+              own[p.width + c + e] = db[i][e];
+            }
+        }
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < 2 * p.width; c += NT) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) s += sums[k * 2 * p.width + c];
+        part[c] = s;
+      }
+      return;
+    }
     for (int k = 0; k < WARPS; ++k) {
       if (int(threadIdx.x / 32) == k && int(threadIdx.x % 32) < TPR) {
 #pragma unroll
@@ -349,26 +376,27 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(NormParam
   }
 }
 
-// Adds the partial rows: 32 columns a block, 32 threads down each column with
-// four sums each, joined in a fixed order.
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int blocks, int width, float* dw, float* db) {
-  __shared__ float sm[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+// Adds the partial rows: 8 columns (a memory sector) a block, 64 threads down each
+// column with four sums each, joined in a fixed order.
+constexpr int kReduceCols = 8, kReduceRows = 64;
+__global__ void __launch_bounds__(kReduceCols * kReduceRows)
+    norm_reduce_kernel(const float* part, int blocks, int width, float* dw, float* db) {
+  __shared__ float sm[kReduceCols][kReduceRows + 1];
+  const int x = threadIdx.x % kReduceCols, y = threadIdx.x / kReduceCols, c = blockIdx.x * kReduceCols + x;
   float s[4] = {};
-  if (c < 2 * width) {
-    int b = threadIdx.y;
-    for (; b + 96 < blocks; b += 128)
+  if (c < 2 * width)
+    for (int b = y; b < blocks; b += 4 * kReduceRows)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += part[size_t(b + 32 * i) * 2 * width + c];
-    for (; b < blocks; b += 32) s[0] += part[size_t(b) * 2 * width + c];
-  }
-  sm[threadIdx.y][threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int i = 0; i < 4; ++i)
+        if (b + i * kReduceRows < blocks) s[i] += part[size_t(b + i * kReduceRows) * 2 * width + c];
+  sm[x][y] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  float v = sm[threadIdx.x][threadIdx.y];   // a warp adds one column
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = blockIdx.x * kReduceCols + warp;
+  if (warp >= kReduceCols) return;
+  float v = sm[warp][lane] + sm[warp][lane + 32];   // a warp adds one column
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < 2 * width) {
+  if (lane == 0 && col < 2 * width) {
     float* out = col < width ? dw : db;
     if (out) out[col < width ? col : col - width] = v;
   }
@@ -448,12 +476,13 @@ int norm_bwd_t(NormParams p, bool want_w, float* d_dw, float* d_db, cudaStream_t
     constexpr int E = decltype(e)::value, TPR = decltype(tpr)::value, V = decltype(v)::value;
     constexpr int NT = norm_threads<TPR>(), ROWS = NT / TPR;
     blocks = norm_blocks(p.n, ROWS);
-    const size_t shm = TPR > 32 || !want_w ? 0 : 2 * size_t(p.width) * sizeof(float);
+    const size_t shm = TPR > 32 || !want_w ? 0 : 2 * size_t(p.width) * sizeof(float) * (norm_side<E, V>() ? NT / 32 : 1);
     norm_bwd_kernel<T, E, TPR, V><<<blocks, NT, shm, st>>>(p);
     return launched();
   });
   if (rc != EGAT_OK || !want_w) return rc;
-  norm_reduce_kernel<<<(2 * p.width + 31) / 32, dim3(32, 32), 0, st>>>(p.part, blocks, p.width, d_dw, d_db);
+  norm_reduce_kernel<<<(2 * p.width + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceRows, 0, st>>>(
+      p.part, blocks, p.width, d_dw, d_db);
   return launched();
 }
 
