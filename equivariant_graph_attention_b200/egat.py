@@ -530,49 +530,43 @@ class MoleculeShape:
                               EGAT_BF16 if self.dtype == "bf16" else EGAT_F32, self.cap)
 
 
-def _typed(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Optional[int]:
-    """The pointer of a contiguous tensor of this type, shape and device; None stays None."""
+def _typed(name: str, t: Optional[torch.Tensor], dtype, shape, device: int) -> Optional[int]:
+    """The pointer of a contiguous tensor of this type, shape and CUDA device; None stays None."""
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"egat: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
+    if t.get_device() != device:
         raise ValueError(f"egat: {name} must live on the CUDA device {device}, not on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"egat: {name} must be contiguous")
     return t.data_ptr()
 
 
-class _on:
-    """The device of a call's tensors as the current one; free where it is already."""
-    __slots__ = ("device", "guard")
-
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise ValueError("egat: tensors must live on a CUDA device")
-        self.device, self.guard = device, None
-
-    def __enter__(self):
-        if torch._C._cuda_getDevice() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _device(t: torch.Tensor) -> int:
+    """The index of a call's CUDA device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("egat: tensors must live on a CUDA device")
+    return dev
 
 
-def _stream_of(stream, device: torch.device) -> int:
+def _elsewhere(dev: int) -> bool:
+    """Whether another device than this one is current."""
+    return torch._C._cuda_getDevice() != dev
+
+
+def _stream_of(stream, dev: int) -> int:
     """The given stream, or the device's current one, as an integer handle."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _scratch(nb: int, workspace: Optional[torch.Tensor], device):
+def _scratch(nb: int, workspace: Optional[torch.Tensor], like: torch.Tensor):
     """The workspace of a call and its size in bytes: the caller's, or a new one if one is needed."""
     if workspace is None:
-        return (torch.empty(nb, dtype=torch.uint8, device=device), nb) if nb else (None, 0)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"egat: workspace must be contiguous on {device}")
+        return (torch.empty(nb, dtype=torch.uint8, device=like.device), nb) if nb else (None, 0)
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"egat: workspace must be contiguous on {like.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -616,18 +610,23 @@ def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tens
     Molecule b: query rows q_ptr[b]:q_ptr[b+1], key rows k_ptr[b]:k_ptr[b+1] (int32 on the
     device; k_ptr None: the queries' own atoms).  Returns (m [nq, D, C] in the storage type,
     lse float32 [nq, H] or None); rows without keys get 0 and -inf."""
-    dev = q.device
-    with _on(dev):
-        ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
-        cs, nb, _ = _mol_call(shape)
-        vals = (shape.nq, shape.D, shape.C)
-        if out is None:
-            out = torch.empty(vals, dtype=shape.torch_dtype, device=dev)
+    dev = _device(q)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return egat_molecule_attention(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, want_lse, out,
+                                           workspace, stream)
+    ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+    cs, nb, _ = _mol_call(shape)
+    vals = (shape.nq, shape.D, shape.C)
+    if out is None:
+        out = q.new_empty(vals)
+        po = out.data_ptr()
+    else:
         po = _typed("out", out, shape.torch_dtype, vals, dev)
-        lse = torch.empty((shape.nq, shape.H), dtype=torch.float32, device=dev) if want_lse else None
-        ws, nb = _scratch(nb, workspace, dev)
-        rc = load_library().egat_molecule_attention(cs, *ptrs, None if ws is None else ws.data_ptr(), nb, po,
-                                                    None if lse is None else lse.data_ptr(), _stream_of(stream, dev))
+    lse = torch.empty((shape.nq, shape.H), dtype=torch.float32, device=q.device) if want_lse else None
+    ws, nb = _scratch(nb, workspace, q)
+    rc = load_library().egat_molecule_attention(cs, *ptrs, None if ws is None else ws.data_ptr(), nb, po,
+                                                None if lse is None else lse.data_ptr(), _stream_of(stream, dev))
     _check("egat_molecule_attention", rc)
     return out, lse
 
@@ -648,32 +647,35 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
     type and (dpos_q, dpos_k, dslope) float32.  In the self form (k_ptr None) dpos_q is the
     whole dL/dr and dpos_k is None; without a slope, or with positions=False (cheaper), the
     last three are None."""
-    dev, T = q.device, shape.torch_dtype
-    with _on(dev):
-        ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
-        cs, _, nb = _mol_call(shape)
-        vals = (shape.nq, shape.D, shape.C)
-        pm, pl, pg = (_typed("m", m, T, vals, dev), _typed("lse", lse, torch.float32, (shape.nq, shape.H), dev),
-                      _typed("grad_m", grad_m, T, vals, dev))
-        ws, nb = _scratch(nb, workspace, dev)
-        dq, dk, dhp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(hp)
-        dpos_q = dpos_k = dslope = None
-        if slope is not None and positions:
-            dpos_q, dslope = torch.empty_like(pos_q), torch.empty_like(slope)
-            dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
-        at = [None if t is None else t.data_ptr() for t in (ws, dq, dk, dhp, dpos_q, dpos_k, dslope)]
-        rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
-                                                             _stream_of(stream, dev))
+    dev, T = _device(q), shape.torch_dtype
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return egat_molecule_attention_backward(shape, q, k, hp, q_ptr, m, lse, grad_m, k_ptr, pos_q, pos_k, slope,
+                                                    positions, workspace, stream)
+    ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
+    cs, _, nb = _mol_call(shape)
+    vals = (shape.nq, shape.D, shape.C)
+    pm, pl, pg = (_typed("m", m, T, vals, dev), _typed("lse", lse, torch.float32, (shape.nq, shape.H), dev),
+                  _typed("grad_m", grad_m, T, vals, dev))
+    ws, nb = _scratch(nb, workspace, q)
+    dq, dk, dhp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(hp)
+    dpos_q = dpos_k = dslope = None
+    if slope is not None and positions:
+        dpos_q, dslope = torch.empty_like(pos_q), torch.empty_like(slope)
+        dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
+    at = [None if t is None else t.data_ptr() for t in (ws, dq, dk, dhp, dpos_q, dpos_k, dslope)]
+    rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
+                                                         _stream_of(stream, dev))
     _check("egat_molecule_attention_backward", rc)
     return dq, dk, dhp, dpos_q, dpos_k, dslope
 
 
-def _norm_rows(name: str, t: torch.Tensor, dtype, shape, device):
+def _norm_rows(name: str, t: torch.Tensor, dtype, shape, device: int):
     """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"egat: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"egat: {name} must live on the CUDA device {device}")
+    if t.get_device() != device:
+        raise ValueError(f"egat: {name} must live on the CUDA device {device}, not on {t.device}")
     n, width = shape
     ld, one = t.stride()
     if width > 1 and one != 1:
@@ -697,18 +699,22 @@ def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     """Layer norm of the rows of x [n, width] (float32 or bf16; any row stride, so h[:, 0, :]
     works in place), weight and bias float32 [width].  Returns (y, stats float32 [n, 2] = mean
     and 1/std, or None).  out may be x itself."""
-    dt, shape, dev, T = _norm_dtype(x), x.shape, x.device, x.dtype
+    dt, dev, shape, T = _norm_dtype(x), _device(x), x.shape, x.dtype
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return egat_layer_norm(x, weight, bias, eps, want_stats, out, stream)
     n, width = shape
-    with _on(dev):
-        px, ldx = _norm_rows("x", x, T, shape, dev)
-        pw = _typed("weight", weight, torch.float32, (width,), dev)
-        pb = _typed("bias", bias, torch.float32, (width,), dev)
-        if out is None:
-            out = torch.empty(shape, dtype=T, device=dev)
+    px, ldx = _norm_rows("x", x, T, shape, dev)
+    pw = _typed("weight", weight, torch.float32, (width,), dev)
+    pb = _typed("bias", bias, torch.float32, (width,), dev)
+    if out is None:
+        out = x.new_empty(shape)
+        py, ldy = (out.data_ptr() if n else None), width
+    else:
         py, ldy = _norm_rows("out", out, T, shape, dev)
-        stats = torch.empty((n, 2), dtype=torch.float32, device=dev) if want_stats else None
-        rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy,
-                                            None if stats is None else stats.data_ptr(), _stream_of(stream, dev))
+    stats = torch.empty((n, 2), dtype=torch.float32, device=x.device) if want_stats else None
+    rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy,
+                                        None if stats is None else stats.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm", rc)
     return out, stats
 
@@ -730,21 +736,24 @@ def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], st
                              workspace: Optional[torch.Tensor] = None, stream=None):
     """(dx in x's type, dweight, dbias float32 [width]) of the layer norm for the upstream
     gradient grad_y; stats as returned by the forward.  out (any row stride) receives dx."""
-    dt, shape, dev, T = _norm_dtype(x), x.shape, x.device, x.dtype
+    dt, dev, shape, T = _norm_dtype(x), _device(x), x.shape, x.dtype
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return egat_layer_norm_backward(x, weight, stats, grad_y, out, workspace, stream)
     n, width = shape
-    with _on(dev):
-        px, ldx = _norm_rows("x", x, T, shape, dev)
-        pg, ldg = _norm_rows("grad_y", grad_y, T, shape, dev)
-        pw = _typed("weight", weight, torch.float32, (width,), dev)
-        ps = _typed("stats", stats, torch.float32, (n, 2), dev)
-        if out is None:
-            out = torch.empty(shape, dtype=T, device=dev)
+    px, ldx = _norm_rows("x", x, T, shape, dev)
+    pg, ldg = _norm_rows("grad_y", grad_y, T, shape, dev)
+    pw = _typed("weight", weight, torch.float32, (width,), dev)
+    ps = _typed("stats", stats, torch.float32, (n, 2), dev)
+    if out is None:
+        out = x.new_empty(shape)
+        po, ldo = (out.data_ptr() if n else None), width
+    else:
         po, ldo = _norm_rows("out", out, T, shape, dev)
-        dw = torch.empty(width, dtype=torch.float32, device=dev)
-        db = torch.empty(width, dtype=torch.float32, device=dev)
-        ws, nb = _scratch(_norm_ws(n, width), workspace, dev)
-        rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg,
-                                                     None if ws is None else ws.data_ptr(), nb, po, ldo,
-                                                     dw.data_ptr(), db.data_ptr(), _stream_of(stream, dev))
+    dw, db = stats.new_empty(width), stats.new_empty(width)
+    ws, nb = _scratch(_norm_ws(n, width), workspace, x)
+    rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg,
+                                                 None if ws is None else ws.data_ptr(), nb, po, ldo,
+                                                 dw.data_ptr(), db.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm_backward", rc)
     return out, dw, db
