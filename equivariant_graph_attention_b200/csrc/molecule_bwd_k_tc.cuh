@@ -15,6 +15,9 @@ template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS, bool POS>
 __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
+  // planes of dS: its terms cancel in the sum, and two planes of bf16 storage take the
+  // rounding of one out of it (1.6 times the error of the result's own rounding)
+  constexpr int DP = PL == 1 ? 2 : 3;
   // the key rows' values as A fragments: in registers, or read again for every
   // step where they would not fit beside the accumulators
   constexpr bool VREG = NT * PL <= 27;
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
             for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
             tc_cap<4, true>(x, fx);
           }
-          uint32_t fd[PL][2][2], fa[PL][2][2];
+          uint32_t fd[DP][2][2], fa[PL][2][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = i >> 1, r = i & 1;
@@ -146,10 +149,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
             if (POS) u[c][r] = f2_fma(ds, slope[h], u[c][r]);
             if constexpr (CAP) ds = f2_mul(ds, fx[i]);
             f2_unpack(ds, a, b);
-            tc_put<PL>(fd, c, r, a, b);
+            tc_put<DP>(fd, c, r, a, b);
           }
           tc_apply<NT, PL>(dv[h], fa, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV);
-          tc_apply<KC, PL>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK);
+          tc_apply<KC, DP>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK);
         }
         if (POS) {
 #pragma unroll

@@ -23,6 +23,9 @@ template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS, bool POS>
 __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3 : 4) : 2) mol_bwd_q_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
+  // planes of dS: its terms cancel in the sum, and two planes of bf16 storage take the
+  // rounding of one out of it (1.6 times the error of the result's own rounding)
+  constexpr int DP = PL == 1 ? 2 : 3;
   constexpr bool FIX = PL == 1;   // m is rounded
   constexpr int SUMS = q_sums(KC, HP, FIX, POS), OUT = HP * KC * 8 + 8;
   extern __shared__ __align__(128) unsigned char tsm[];
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
             for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
             tc_cap<4, true>(x, fx);
           }
-          uint32_t fd[PL][2][2], fa[PL][2][2];
+          uint32_t fd[DP][2][2], fa[PL][2][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = i >> 1, r = i & 1;
@@ -205,11 +208,11 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
               f2_unpack(w, a, b);
             }
             f2_unpack(ds, lo, hi);
-            tc_put<PL>(fd, c, r, lo, hi);
+            tc_put<DP>(fd, c, r, lo, hi);
             if (FIX) tc_put<PL>(fa, c, r, a, b);
           }
           const uint32_t kb = st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16);
-          tc_apply<KC, PL>(dq[h], fd, kb, 16, L::PK);
+          tc_apply<KC, DP>(dq[h], fd, kb, 16, L::PK);
           if constexpr (FIX) tc_apply<KC, PL>(bk[h], fa, kb, 16, L::PK);
         }
         if constexpr (POS) {

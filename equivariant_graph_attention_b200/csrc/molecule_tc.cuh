@@ -407,15 +407,16 @@ __device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[P
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.f;
   }
+  // small products first: a tensor-core sum drops bits below its largest term
 #pragma unroll
-  for (int q = 0; q < PL; ++q) {
+  for (int q = PL - 1; q >= 0; --q) {
 #pragma unroll
     for (int c = 0; c + 1 < NC; c += 2) {
       uint32_t b[4];
       tc_ldsm4(base + q * plane + c * step, b);
 #pragma unroll
-      for (int k = 0; k < PL - q; ++k) {
-        if (c == 0 && q == 0 && k == 0 && !ADD) {
+      for (int k = PL - 1 - q; k >= 0; --k) {
+        if (c == 0 && q == PL - 1 && !ADD) {
           tc_mma16_first(acc[0], a[k][c], a[k][c + 1], b[0], b[1]);
           tc_mma16_first(acc[1], a[k][c], a[k][c + 1], b[2], b[3]);
         } else {
@@ -428,7 +429,7 @@ __device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[P
       uint32_t b0, b1;
       tc_ldsm2(base2 + q * plane + (NC - 1) * step, b0, b1);
 #pragma unroll
-      for (int k = 0; k < PL - q; ++k) {
+      for (int k = PL - 1 - q; k >= 0; --k) {
         tc_mma8(acc[0], a[k][NC - 1], b0);
         tc_mma8(acc[1], a[k][NC - 1], b1);
       }
@@ -437,27 +438,68 @@ __device__ __forceinline__ void tc_dot(float (&acc)[2][4], const uint32_t (&a)[P
 }
 // acc[NC chunks of columns] += w (16 rows x 16 other rows) . other rows; base is
 // the lane's address of chunk 0 for a transposed x4 load (row by lane & 15,
-// chunk by lane / 16).
-template <int NC, int PL>
-__device__ __forceinline__ void tc_apply(float (&acc)[NC][4], const uint32_t (&w)[PL][2][2], uint32_t base, int step,
+// chunk by lane / 16).  PW planes of w; of the rows as many for float32, one for bf16.
+// For float32 a step's products are summed apart, small ones first, and added to
+// the accumulator by the FMA pipe, which rounds where the tensor core truncates:
+// the many steps of a long molecule added up to 2e-6 of the result otherwise.
+template <int NC, int PW>
+__device__ __forceinline__ void tc_apply(float (&acc)[NC][4], const uint32_t (&w)[PW][2][2], uint32_t base, int step,
                                          int plane) {
-#pragma unroll
-  for (int q = 0; q < PL; ++q) {
+  if constexpr (PW < 3) {
 #pragma unroll
     for (int c = 0; c + 1 < NC; c += 2) {
       uint32_t b[4];
-      tc_ldsm4t(base + q * plane + c * step, b);
+      tc_ldsm4t(base + c * step, b);
 #pragma unroll
-      for (int k = 0; k < PL - q; ++k) {
+      for (int k = PW - 1; k >= 0; --k) {
         tc_mma16(acc[c], w[k][0], w[k][1], b[0], b[1]);
         tc_mma16(acc[c + 1], w[k][0], w[k][1], b[2], b[3]);
       }
     }
     if constexpr (NC & 1) {
       uint32_t b0, b1;
-      tc_ldsm2t(base + q * plane + (NC - 1) * step, b0, b1);
+      tc_ldsm2t(base + (NC - 1) * step, b0, b1);
 #pragma unroll
-      for (int k = 0; k < PL - q; ++k) tc_mma16(acc[NC - 1], w[k][0], w[k][1], b0, b1);
+      for (int k = PW - 1; k >= 0; --k) tc_mma16(acc[NC - 1], w[k][0], w[k][1], b0, b1);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c + 1 < NC; c += 2) {
+      float t[2][4];
+#pragma unroll
+      for (int q = 2; q >= 0; --q) {
+        uint32_t b[4];
+        tc_ldsm4t(base + q * plane + c * step, b);
+#pragma unroll
+        for (int k = 2 - q; k >= 0; --k) {
+          if (q == 2) {
+            tc_mma16_first(t[0], w[k][0], w[k][1], b[0], b[1]);
+            tc_mma16_first(t[1], w[k][0], w[k][1], b[2], b[3]);
+          } else {
+            tc_mma16(t[0], w[k][0], w[k][1], b[0], b[1]);
+            tc_mma16(t[1], w[k][0], w[k][1], b[2], b[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[c + (i >> 2)][i & 3] += t[i >> 2][i & 3];
+    }
+    if constexpr (NC & 1) {
+      float t[4];
+#pragma unroll
+      for (int q = 2; q >= 0; --q) {
+        uint32_t b0, b1;
+        tc_ldsm2t(base + q * plane + (NC - 1) * step, b0, b1);
+#pragma unroll
+        for (int k = 2 - q; k >= 0; --k) {
+          if (q == 2)
+            tc_mma16_first(t, w[k][0], w[k][1], b0, b1);
+          else
+            tc_mma16(t, w[k][0], w[k][1], b0, b1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[NC - 1][i] += t[i];
     }
   }
 }
