@@ -32,12 +32,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
   const size_t rowA = size_t(t.row0) + rA, rowB = rowA + 8;
   const uint32_t sbase = tc_smem(tsm);
   TcLoader<NT, KC, HP, PL> ld;
+  // a stage, with minus lse2 and delta of the query rows; no weight past the molecule
   auto load = [&](int r0, int b) {
     const uint32_t st = sbase + b * L::STAGE;
     ld.load(st, t.o1 - r0);
-    // minus lse2 and delta of the query rows; no weight past the molecule
     for (int i = threadIdx.x; i < kTcStage * HP; i += kTcThreads) {
-      const int r = i / HP, h = i % HP, o = L::ROW + (h * 2 * kTcStage + r) * 4;
+      const int r = i / HP, h = i % HP, o = (PL == 1 ? L::ROW : L::RAWP + kTcStage * 12) + (h * 2 * kTcStage + r) * 4;
       const size_t at = size_t(r0 + r) * p.H + head0 + h;
       if (r0 + r < t.o1) {
         tc_cp4(st + o, p.nlse2 + at, true);
@@ -48,6 +48,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
       }
     }
   };
+  auto split = [&](int left) {
+    ld.split(sbase, left);
+    for (int r = threadIdx.x; r < kTcStage; r += kTcThreads)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        tc_move4(sbase + L::ROW + (e * kTcStage + r) * 4, sbase + L::RAWP + kTcStage * 12 + (e * kTcStage + r) * 4);
+  };
   // its own rows of k and h' pass through the stage that the queries take last
   const uint32_t own = sbase + (L::BUFS - 1) * L::STAGE, own_rows = rw * 16;
   {
@@ -55,11 +62,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
     rows.init(p, p.a.k, p.a.hp, nullptr, head0, t.row0);
     rows.pos = nullptr;
     rows.load(own, t.rows);
+    tc_commit();
+    if constexpr (L::BUFS == 1) {
+      tc_wait<0>();
+      rows.split(own, t.rows);
+    }
   }
-  tc_commit();
   if (t.o0 < t.o1) {
     ld.init(p, p.a.q, p.g.g, p.a.posq, head0, t.o0);
-    if (L::BUFS == 2) load(t.o0, 0);
+    load(t.o0, 0);
   }
   tc_commit();
 
@@ -90,12 +101,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
   __syncthreads();   // the loop fills that stage
   int buf = 0;
   for (int q0 = t.o0; q0 < t.o1; q0 += kTcStage, buf ^= L::BUFS - 1) {
-    if (L::BUFS == 1)
-      load(q0, 0);
-    else if (q0 + kTcStage < t.o1)
-      load(q0 + kTcStage, buf ^ 1);
-    tc_commit();
-    tc_wait<L::BUFS - 1>();
+    if constexpr (L::BUFS == 2) {
+      if (q0 + kTcStage < t.o1) load(q0 + kTcStage, buf ^ 1);
+      tc_commit();
+      tc_wait<1>();
+    } else {
+      tc_wait<0>();
+      split(t.o1 - q0);
+      if (q0 + kTcStage < t.o1) load(q0 + kTcStage, 0);
+      tc_commit();
+    }
     __syncthreads();
     const uint32_t st = sbase + buf * L::STAGE;
     const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
@@ -234,7 +249,7 @@ int tc_backward_k(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 2>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
-    const int shm = std::max({L::BUFS * L::STAGE, tc_join_bytes(HP * (NT + KC) * 4 + 6),
+    const int shm = std::max({L::BYTES, tc_join_bytes(HP * (NT + KC) * 4 + 6),
                               int(64 * (L::OUTROW + HP * KC * 8 + 8) * sizeof(typename L::T))});
     const dim3 grid(mol_slots(p.nk, p.nmol, 16 << p.rwlog), p.H / HP);
     // positions come with a bias

@@ -48,8 +48,12 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
     rows.init(p, p.a.q, p.g.g, nullptr, head0, t.row0);
     rows.pos = nullptr;
     rows.load(own, t.rows);
+    tc_commit();
+    if constexpr (L::BUFS == 1) {
+      tc_wait<0>();
+      rows.split(own, t.rows);
+    }
   }
-  tc_commit();
   TcLoader<NT, KC, HP, PL> ld;
   if (t.o0 < t.o1) {
     ld.init(p, p.a.k, p.a.hp, p.a.posk, head0, t.o0);
@@ -72,10 +76,11 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
     TcPart<HP * NT, PL> rows;
     const int c = lane % (HP * NT);
     rows.init(static_cast<const T*>(p.g.m), p.D * p.C, tc_val_off(p, head0 + c % HP, c / HP), t.row0, L::VAL, L::RV);
-    rows.template load<L::RV>(own, t.rows, true);
+    rows.template load<L::RV>(L::BUFS == 2 ? own : own + L::RAWV, t.rows, true);
+    tc_commit();
+    tc_wait<0>();
+    if constexpr (L::BUFS == 1) rows.template split<L::RV>(own, own + L::RAWV, t.rows);
   }
-  tc_commit();
-  tc_wait<0>();
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < HP; ++h) {
@@ -127,15 +132,21 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
   f32x2 gs[2][3] = {}, ga[HP][2][3] = {};
   f32x2 sd[HP][2] = {}, sa[HP][2] = {};
 
+  if (L::BUFS == 1 && t.o0 < t.o1) ld.load(sbase, t.o1 - t.o0);
+  tc_commit();
   __syncthreads();   // the loop fills that stage
   int buf = 0;
   for (int k0 = t.o0; k0 < t.o1; k0 += kTcStage, buf ^= L::BUFS - 1) {
-    if (L::BUFS == 1)
-      ld.load(sbase, t.o1 - k0);
-    else if (k0 + kTcStage < t.o1)
-      ld.load(sbase + (buf ^ 1) * L::STAGE, t.o1 - k0 - kTcStage);
-    tc_commit();
-    tc_wait<L::BUFS - 1>();
+    if constexpr (L::BUFS == 2) {
+      if (k0 + kTcStage < t.o1) ld.load(sbase + (buf ^ 1) * L::STAGE, t.o1 - k0 - kTcStage);
+      tc_commit();
+      tc_wait<1>();
+    } else {
+      tc_wait<0>();
+      ld.split(sbase, t.o1 - k0);
+      if (k0 + kTcStage < t.o1) ld.load(sbase, t.o1 - k0 - kTcStage);
+      tc_commit();
+    }
     __syncthreads();
     const uint32_t st = sbase + buf * L::STAGE;
     const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
@@ -360,7 +371,7 @@ int tc_backward_q(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 1>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
-    const int shm = std::max({L::BUFS * L::STAGE, tc_join_bytes(q_sums(KC, HP, PL == 1, true)),
+    const int shm = std::max({L::BYTES, tc_join_bytes(q_sums(KC, HP, PL == 1, true)),
                               int(64 * (HP * KC * 8 + 8) * sizeof(typename L::T))});
     const dim3 grid(p.slots, p.H / HP);
     // positions come with a bias

@@ -38,13 +38,17 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
     const int c = lane % (HP * KC);
     const bool have = (c % KC) * 8 < p.dk;
     rows.init(static_cast<const T*>(p.a.q), p.H * p.dk, (head0 + c / KC) * p.dk + (have ? c % KC : 0) * 8, t.row0, L::QK, L::RK);
-    rows.template load<L::RK>(own, t.rows, have);
+    rows.template load<L::RK>(L::BUFS == 2 ? own : own + L::STAGE, t.rows, have);
+    tc_commit();
+    if constexpr (L::BUFS == 1) {
+      tc_wait<0>();
+      rows.template split<L::RK>(own, own + L::STAGE, t.rows);
+    }
   }
-  tc_commit();
   TcLoader<NT, KC, HP, PL> ld;
   if (k_begin < k_end) {
     ld.init(p, p.a.k, p.a.hp, p.a.posk, head0, k_begin);
-    if (L::BUFS == 2) ld.load(sbase, k_end - k_begin);
+    ld.load(sbase, k_end - k_begin);
   }
   tc_commit();
 
@@ -80,12 +84,16 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
   int buf = 0;
   bool first = true;
   for (int k0 = k_begin; k0 < k_end; k0 += kTcStage, buf ^= L::BUFS - 1) {
-    if (L::BUFS == 1)
-      ld.load(sbase, k_end - k0);
-    else if (k0 + kTcStage < k_end)
-      ld.load(sbase + (buf ^ 1) * L::STAGE, k_end - k0 - kTcStage);
-    tc_commit();
-    tc_wait<L::BUFS - 1>();
+    if constexpr (L::BUFS == 2) {
+      if (k0 + kTcStage < k_end) ld.load(sbase + (buf ^ 1) * L::STAGE, k_end - k0 - kTcStage);
+      tc_commit();
+      tc_wait<1>();
+    } else {
+      tc_wait<0>();
+      ld.split(sbase, k_end - k0);
+      if (k0 + kTcStage < k_end) ld.load(sbase, k_end - k0 - kTcStage);
+      tc_commit();
+    }
     __syncthreads();
     const uint32_t st = sbase + buf * L::STAGE;
     const float* sp = reinterpret_cast<const float*>(tsm + buf * L::STAGE + L::POS);
@@ -280,7 +288,7 @@ int tc_forward(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 2>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {
     constexpr int NT = decltype(nt)::value, KC = decltype(kc)::value, HP = decltype(hp)::value;
     using L = TcLay<NT, KC, HP, PL>;
-    const size_t shm = std::max(L::BUFS * L::STAGE, 4 * 16 * (L::OUTROW + 2 * HP) * 4);
+    const size_t shm = std::max(L::BYTES, 4 * 16 * (L::OUTROW + 2 * HP) * 4);
     const dim3 grid(p.slots, p.H / HP, p.splits);
     return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
       return tc_launch(mol_fwd_tc_kernel<NT, KC, HP, PL, decltype(cap)::value, decltype(bias)::value>, grid, shm, p, st);

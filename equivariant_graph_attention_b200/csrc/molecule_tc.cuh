@@ -20,8 +20,8 @@
 // the six bf16 products whose planes add up to two at most; what is left out is
 // below 2^-25 of the terms.  Six products at the tensor rate are four thirds of the
 // FMA pipe's rate, without its shared-memory reads (216-water box: 107 us on that
-// pipe).  These stages are converted on their way in, so they are not copied
-// asynchronously, and a warp takes one head.
+// pipe).  A stage is copied as it is while the last one is worked on, and each lane then
+// splits what it copied; a warp takes one head.
 #pragma once
 
 #include <algorithm>
@@ -51,7 +51,11 @@ struct TcLay {
   static constexpr int POS = VAL + kTcStage * RV;    // x[64], y[64], z[64]
   static constexpr int ROW = POS + kTcStage * 12;    // per head: lse2[64], delta[64]
   static constexpr int STAGE = ROW + HP * kTcStage * 8;
-  static constexpr int BUFS = PL == 1 ? 2 : 1;       // asynchronous copies alone need two stages
+  // float32: one split stage, and behind it what was copied: rows of both parts, then
+  // positions and row numbers
+  static constexpr int BUFS = PL == 1 ? 2 : 1;
+  static constexpr int RAWV = STAGE + kTcStage * KC * 32, RAWP = RAWV + kTcStage * NT * 32;
+  static constexpr int BYTES = PL == 1 ? 2 * STAGE : RAWP + kTcStage * 20;   // all stages
   static constexpr int OUTROW = HP * NT * 8 + 8;     // floats of a joined row (bank spread)
 };
 
@@ -62,6 +66,9 @@ __device__ __forceinline__ void tc_cp16(uint32_t dst, const void* src, bool ok) 
 }
 __device__ __forceinline__ void tc_cp4(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void tc_move4(uint32_t to, uint32_t from) {
+  asm volatile("{\n .reg .b32 x;\n ld.shared.b32 x, [%1];\n st.shared.b32 [%0], x;\n}\n" ::"r"(to), "r"(from) : "memory");
 }
 __device__ __forceinline__ void tc_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
@@ -167,52 +174,55 @@ struct TcPart {
     src = base + size_t(r0 + r) * ld + off;
     dst = at + r * rs + (lane % W) * 16;
   }
+  // bf16: into a stage; float32: as it is, 32 bytes a chunk, to `st`
   template <int RS>
   __device__ __forceinline__ void load(uint32_t st, int left, bool have) {
     const int need = (left + 15) & ~15;   // rows that the last step of 16 meets
-    if constexpr (PL == 1) {
-      if (row < kTcStage) {
-        if (left >= kTcStage && have) {
+    if (row < kTcStage) {
+      if (PL == 1 && left >= kTcStage && have) {
 #pragma unroll
-          for (int i = 0; i < ITS; ++i)
-            if (kTcStage % STEP == 0 || row + i * STEP < kTcStage)
-              tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
-        } else {
+        for (int i = 0; i < ITS; ++i)
+          if (kTcStage % STEP == 0 || row + i * STEP < kTcStage)
+            tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, true);
+      } else {
 #pragma unroll
-          for (int i = 0; i < ITS; ++i)
-            if (i * STEP < need && (kTcStage % STEP == 0 || row + i * STEP < kTcStage))
-              tc_cp16(st + dst + i * STEP * RS, src + size_t(i) * STEP * ld, have && row + i * STEP < left);
-        }
-      }
-    } else {
-      constexpr int AT_ONCE = ITS < 4 ? ITS : 4;   // rows on their way together
-#pragma unroll 1
-      for (int i0 = 0; i0 * STEP < need && i0 < ITS; i0 += AT_ONCE) {
-        float4 v[AT_ONCE][2];
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-          const bool ok = have && row + (i0 + i) * STEP < min(left, kTcStage);
-          const float4* x = reinterpret_cast<const float4*>(src + size_t(i0 + i) * STEP * ld);
-          v[i][0] = ok ? __ldg(x) : make_float4(0.f, 0.f, 0.f, 0.f);
-          v[i][1] = ok ? __ldg(x + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-          if (row + (i0 + i) * STEP >= kTcStage) continue;
-          uint32_t w[4][PL];
-          tc_planes<PL>(v[i][0].x, v[i][0].y, w[0]);
-          tc_planes<PL>(v[i][0].z, v[i][0].w, w[1]);
-          tc_planes<PL>(v[i][1].x, v[i][1].y, w[2]);
-          tc_planes<PL>(v[i][1].z, v[i][1].w, w[3]);
-#pragma unroll
-          for (int k = 0; k < PL; ++k)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(st + dst + (i0 + i) * STEP * RS + k * W * 16),
-                         "r"(w[0][k]), "r"(w[1][k]), "r"(w[2][k]), "r"(w[3][k])
-                         : "memory");
-        }
+        for (int i = 0; i < ITS; ++i)
+          if (i * STEP < need && (kTcStage % STEP == 0 || row + i * STEP < kTcStage)) {
+            const bool ok = have && row + i * STEP < left;
+            const T* x = src + size_t(i) * STEP * ld;
+            if constexpr (PL == 1) {
+              tc_cp16(st + dst + i * STEP * RS, x, ok);
+            } else {
+              const uint32_t to = st + ((row + i * STEP) * W + (threadIdx.x & 31) % W) * 32;
+              tc_cp16(to, x, ok);
+              tc_cp16(to + 16, x + 4, ok);
+            }
+          }
       }
     }
     src += size_t(kTcStage) * ld;
+  }
+  // float32: what this lane copied to `raw`, split, into the stage at st
+  template <int RS>
+  __device__ __forceinline__ void split(uint32_t st, uint32_t raw, int left) const {
+    const int need = (left + 15) & ~15;
+    if (row < kTcStage)
+#pragma unroll 2
+      for (int i = 0; i < ITS; ++i) {
+        if (i * STEP >= need || row + i * STEP >= kTcStage) break;
+        const uint32_t from = raw + ((row + i * STEP) * W + (threadIdx.x & 31) % W) * 32;
+        float v[8];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(from) : "memory");
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(from + 16) : "memory");
+        uint32_t w[4][PL];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tc_planes<PL>(v[2 * e], v[2 * e + 1], w[e]);
+#pragma unroll
+        for (int k = 0; k < PL; ++k)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(st + dst + i * STEP * RS + k * W * 16),
+                       "r"(w[0][k]), "r"(w[1][k]), "r"(w[2][k]), "r"(w[3][k])
+                       : "memory");
+      }
   }
 };
 template <int NT, int KC, int HP, int PL>
@@ -232,16 +242,29 @@ struct TcLoader {
     val.init(static_cast<const T*>(v), p.D * p.C, tc_val_off(p, head0 + cv % HP, cv / HP), r0, L::VAL, L::RV);
     pos = p.a.slope ? positions + size_t(r0) * 3 : nullptr;
   }
+  // bf16: the next stage to st; float32: to the copies' place behind the stage at st
   __device__ __forceinline__ void load(uint32_t st, int left) {
-    qk.template load<L::RK>(st, left, have);
-    val.template load<L::RV>(st, left, true);
+    qk.template load<L::RK>(PL == 1 ? st : st + L::STAGE, left, have);
+    val.template load<L::RV>(PL == 1 ? st : st + L::RAWV, left, true);
     if (pos) {
       const int c = threadIdx.x >> 5;
       if (c < 3)
 #pragma unroll
         for (int r = threadIdx.x & 31; r < kTcStage; r += 32)
-          tc_cp4(st + L::POS + c * (kTcStage * 4) + r * 4, r < left ? pos + r * 3 + c : pos, r < left);
+          tc_cp4(st + (PL == 1 ? L::POS : L::RAWP) + c * (kTcStage * 4) + r * 4, r < left ? pos + r * 3 + c : pos, r < left);
       pos += kTcStage * 3;
+    }
+  }
+  // float32: the copies (complete for this thread) into the stage at st
+  __device__ __forceinline__ void split(uint32_t st, int left) const {
+    if constexpr (PL == 3) {
+      qk.template split<L::RK>(st, st + L::STAGE, left);
+      val.template split<L::RV>(st, st + L::RAWV, left);
+      if (pos && threadIdx.x < 96)
+#pragma unroll
+        for (int r = threadIdx.x & 31; r < kTcStage; r += 32)
+          tc_move4(st + L::POS + (threadIdx.x >> 5) * (kTcStage * 4) + r * 4,
+                   st + L::RAWP + (threadIdx.x >> 5) * (kTcStage * 4) + r * 4);
     }
   }
 };
@@ -253,15 +276,6 @@ __device__ __forceinline__ void tc_load2(const __nv_bfloat16* x, bool ok, uint32
 __device__ __forceinline__ void tc_load2(const float* x, bool ok, uint32_t (&w)[3]) {
   const float2 v = ok ? __ldg(reinterpret_cast<const float2*>(x)) : make_float2(0.f, 0.f);
   tc_planes<3>(v.x, v.y, w);
-}
-// ... and as float32
-__device__ __forceinline__ float2 tc_float2(const __nv_bfloat16* x, bool ok) {
-  float2 v;
-  f2_unpack(bf16x2_to_f2(ok ? __ldg(reinterpret_cast<const uint32_t*>(x)) : 0u), v.x, v.y);
-  return v;
-}
-__device__ __forceinline__ float2 tc_float2(const float* x, bool ok) {
-  return ok ? __ldg(reinterpret_cast<const float2*>(x)) : make_float2(0.f, 0.f);
 }
 __device__ __forceinline__ void tc_store2(__nv_bfloat16* x, float a, float b) {
   *reinterpret_cast<uint32_t*>(x) = tc_pack(a, b);
@@ -278,21 +292,6 @@ __device__ __forceinline__ void tc_store8(float* x, const float (&v)[8]) {
 }
 
 // A fragments of this lane's rows (r0 = row g, r1 = row g + 8) from global memory
-template <int KC, int PL>
-__device__ __forceinline__ void tc_frag_qk(const MolParams& p, const void* src, size_t r0, size_t r1, bool l0, bool l1,
-                                           int head, uint32_t (&f)[PL][KC][2]) {
-  const typename TcStorage<PL>::T* x = static_cast<const typename TcStorage<PL>::T*>(src);
-  const int kc = p.dk >> 3, t2 = (threadIdx.x & 3) * 2;
-#pragma unroll
-  for (int c = 0; c < KC; ++c)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint32_t w[PL];
-      tc_load2(x + ((r ? r1 : r0) * p.H + head) * p.dk + c * 8 + t2, (r ? l1 : l0) && c < kc, w);
-#pragma unroll
-      for (int k = 0; k < PL; ++k) f[k][c][r] = w[k];
-    }
-}
 template <int NT, int PL>
 __device__ __forceinline__ void tc_frag_val(const MolParams& p, const void* src, size_t r0, size_t r1, bool l0, bool l1,
                                             int head, uint32_t (&f)[PL][NT][2], int c0 = 0) {
