@@ -15,6 +15,7 @@ import hashlib
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -45,21 +46,29 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
                      + glob.glob(os.path.join(INCLUDE, "*.h")))
     flags = CFLAGS + (["-Xptxas", "-v"] if ptxas_info else [])
-    objs = []
+    objs, jobs = [], []
     for src in sources:
         tag = _digest([src] + headers, flags)
         obj = os.path.join(BUILD, f"{os.path.basename(src)}.{tag}.o")
         objs.append(obj)
-        if os.path.exists(obj) and not ptxas_info:
-            continue
+        if not os.path.exists(obj) or ptxas_info:
+            jobs.append((src, obj))
+
+    def compile_one(job):
+        src, obj = job
         cmd = [NVCC] + flags + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0 or verbose or ptxas_info:
-            sys.stderr.write(r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}")
+        return src, subprocess.run(cmd, capture_output=True, text=True)
+
+    # the sources are compiled side by side: the templates of the attention within
+    # molecules take a minute each
+    with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+        for src, r in pool.map(compile_one, jobs):
+            if r.returncode != 0 or verbose or ptxas_info:
+                sys.stderr.write(r.stdout + r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed on {src}")
     link_tag = _digest(objs, ARCH)
     stamp = os.path.join(BUILD, "libegat.stamp")
     if os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == link_tag:

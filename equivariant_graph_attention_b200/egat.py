@@ -561,6 +561,14 @@ def _stream_of(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _used_on(stream, *tensors) -> None:
+    """Memory that a call allocated on the current stream is also in use on the stream it was given."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _scratch(nb: int, workspace: Optional[torch.Tensor], like: torch.Tensor):
     """The workspace of a call and its size in bytes: the caller's, or a new one if one is needed."""
     if workspace is None:
@@ -628,6 +636,7 @@ def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tens
     rc = load_library().egat_molecule_attention(cs, *ptrs, None if ws is None else ws.data_ptr(), nb, po,
                                                 None if lse is None else lse.data_ptr(), _stream_of(stream, dev))
     _check("egat_molecule_attention", rc)
+    _used_on(stream, out, lse, ws)
     return out, lse
 
 
@@ -667,6 +676,7 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
     rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
                                                          _stream_of(stream, dev))
     _check("egat_molecule_attention_backward", rc)
+    _used_on(stream, ws, dq, dk, dhp, dpos_q, dpos_k, dslope)
     return dq, dk, dhp, dpos_q, dpos_k, dslope
 
 
@@ -716,6 +726,7 @@ def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy,
                                         None if stats is None else stats.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm", rc)
+    _used_on(stream, out, stats)
     return out, stats
 
 
@@ -756,4 +767,5 @@ def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], st
                                                  None if ws is None else ws.data_ptr(), nb, po, ldo,
                                                  dw.data_ptr(), db.data_ptr(), _stream_of(stream, dev))
     _check("egat_layer_norm_backward", rc)
+    _used_on(stream, out, dw, db, ws)
     return out, dw, db
