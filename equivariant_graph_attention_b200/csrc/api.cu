@@ -306,7 +306,7 @@ static int check_mol_shape(const egat_mol_shape* s) {
   if (!s) return EGAT_ERR_ARG;
   if (s->nq < 0 || s->nk < 0 || s->n_mol < 0) return EGAT_ERR_ARG;
   if (s->dtype != EGAT_F32 && s->dtype != EGAT_BF16) return EGAT_ERR_ARG;
-  if (s->cap != 0.f && !(s->cap >= 1e-30f && s->cap <= 3.0e38f)) return EGAT_ERR_ARG;
+  if (s->cap != 0.f && !(s->cap >= 1e-30f && s->cap <= 1e30f)) return EGAT_ERR_ARG;
   if (s->lmax < 0 || s->lmax > kMaxL) return EGAT_ERR_UNSUPPORTED;
   if (s->C != 16 && s->C != 32 && s->C != 64 && s->C != 128) return EGAT_ERR_UNSUPPORTED;
   if (!pow2(s->H) || s->C % s->H != 0 || (s->C / s->H) % 8 != 0) return EGAT_ERR_UNSUPPORTED;

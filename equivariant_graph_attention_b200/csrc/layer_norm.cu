@@ -9,6 +9,9 @@
 // threads share a row: part of a warp up to 32 vectors, a warp up to 1,024
 // columns, a block beyond.  Vectors are 16 bytes of bf16 (two of float32)
 // where width, strides and pointers allow, pairs or single elements otherwise.
+// A thread keeps its columns' weight and bias over the rows that it visits and has
+// the next row on its way (100,000 x 1,000 bf16 rows: 74 us, 82 % of the measured copy
+// rate; 209 us with both read again for every row, a block a row).
 //
 // The weight sums of the backward pass: each thread keeps its columns' sums
 // over the rows its block visits, the block joins its rows' groups in a fixed

@@ -1,17 +1,20 @@
-// Attention within each molecule, forward and backward, for every shape and
-// storage type on the FMA pipe in float32, and the host side: which kernels a
-// shape takes, key splits, workspaces.
+// Attention within each molecule, forward and backward: the host side (which
+// kernels a shape takes, tiles, key splits, workspaces), the join of key splits,
+// the position and slope sums, and the kernels on the FMA pipe in float32 for the
+// shapes that the tensor-core kernels leave (more than 256 value columns a head of
+// bf16, 144 of float32; one head of bf16 with few columns).
 //
 //   x_ij = q_i.k_j / sqrt(dk),  s_ij = f(x_ij) - slope |r_i - r_j|,
 //   f(x) = x or cap tanh(x / cap),  m_i = sum_j softmax_j(s_ij) h'_j
 //
-// The rows of one head are taken in tiles of one molecule (molecule.cuh); a
-// group of LP lanes holds a row: its query, its accumulators and, backward,
-// its gradient, split over the lanes in float4 vectors.  Key (or, for the
-// gradients of the keys, query) rows pass through shared memory as float32
-// and are read by broadcast, so a warp's read serves 32 / LP rows.  The
-// softmax runs online with base-2 exponents: one running maximum and sum per
-// row, rescaled only when the maximum grows.
+// In the FMA kernels the rows of one head are taken in tiles of one molecule
+// (molecule.cuh); a group of LP lanes holds a row: its query, its accumulators and,
+// backward, its gradient, split over the lanes in float4 vectors.  Key (or, for
+// the gradients of the keys, query) rows pass through shared memory as float32 and
+// are read by broadcast, so a warp's read serves 32 / LP rows.  The softmax runs
+// online with base-2 exponents: one running maximum and sum per row, rescaled only
+// when the maximum grows.  They are bound by shared-memory reads: a 16-byte read
+// feeds four products, a quarter of what the FMA pipe could take.
 #include <cmath>
 
 #include "molecule.cuh"

@@ -7,6 +7,10 @@
 namespace egat {
 namespace {
 
+// Bound by latency at two blocks an SM: the accumulators and the key rows' fragments
+// fill the registers (4,096 atoms capped: 0.65 ms, a third of the tensor pipe and of
+// the issue slots).
+//
 // dL/dk, dL/dh' and, with POS, the key side of dL/dr: a warp owns 16 key rows
 // and meets the molecule's query rows.  The products are transposed (S^T = K Q^T,
 // dP^T = H' G^T), so that the weights and dS land as the A operands of

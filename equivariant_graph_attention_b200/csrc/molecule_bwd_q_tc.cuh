@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
 }
 
 // One head a warp at 72 columns: three or four blocks an SM instead of two (4,096
-// atoms capped: 0.61 -> 0.55 ms; the key side and the forward pass lose by it).
+// atoms capped: 0.61 -> 0.52 ms; the key side and the forward pass lose by it).  Bound
+// by instruction issue and latency: half of the issue slots are busy, a quarter of
+// the tensor pipe.
 template <int PL>
 int tc_backward_q(const MolParams& p, cudaStream_t st) {
   return tc_dispatch<PL, 1>(p.dv / 8, p.dk, [&](auto nt, auto kc, auto hp) {

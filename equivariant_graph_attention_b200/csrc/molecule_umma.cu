@@ -10,14 +10,16 @@
 //    memory, where it replaces the scores;
 //  * a row of a group is two threads', of two warps that share its lanes: each
 //    reads 32 of its 64 scores, applies cap, bias and exponential, and writes its
-//    weights back as bf16.  (One thread with all 64 left two warps a scheduler,
-//    which waited most of the time: 0.71 ms at 8,191 atoms and lmax 3.)  The row's
+//    weights back as bf16.  (One thread with all 64 leaves two warps a scheduler to
+//    hide each other's latency: 0.40 instead of 0.37 ms at 4,096 capped atoms.)  The row's
 //    reference moves only when a score passes it by 2^8; only then do the two
 //    exchange their maxima, and the accumulator is rescaled in place.
 // While a group works on one stage, the tensor core forms its next scores and
 // the other group's products.  Work per pair and head is one exponential (and one
-// root with a bias) on the special-function unit, which is what bounds it: the
-// products take a quarter of that at 16 + 72 columns.  Every wait is bounded.
+// root with a bias) on the special-function unit, which bounds it without a cap
+// (8,191 atoms, lmax 3: 0.24 of 0.48 ms); cap and bias add 13 operations on the FMA
+// pipe and bound it there (4,096 atoms, lmax 2: 0.17 of 0.37 ms).  The products take
+// about a third of the exponentials' time at 16 + 72 columns.  Every wait is bounded.
 #include <algorithm>
 
 #include "molecule_umma.cuh"

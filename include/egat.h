@@ -404,10 +404,11 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  * atoms) attend to long systems; the keys are then split over the GPU and
  * joined.  A row of no molecule (before the first or behind the last) and a
  * row whose molecule has no keys get m = 0 and lse = -inf; rows of other
- * molecules never reach a row's result, not even as NaN.
+ * molecules never reach a row's result, not even as NaN.  A score of -inf (an
+ * infinite distance) masks its pair; a row of nothing else is an empty row.
  *  s->lmax  0..3 (0: plain scalar values), C, H, dk as in the module header;
  *           lmax, C and H split the values by head as in step 3
- *  s->cap   0 = no cap; from 1e-30 to 3e38 otherwise
+ *  s->cap   0 = no cap; from 1e-30 to 1e30 otherwise
  *  d_q [nq][H][dk], d_k [nk][H][dk], d_hp [nk][D][C] in s->dtype
  *  d_pos_q, d_pos_k float32 [nq][3], [nk][3]; d_slope float32 [H], any sign:
  *           all used if d_slope is not NULL, none otherwise
@@ -415,10 +416,16 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  *           the value products as bf16, so a wider result would not hold more)
  *  d_lse    float32 [nq][H], natural logarithm; may be NULL (the backward
  *           pass needs it)
- *  d_ws     at least egat_molecule_attention_workspace_bytes(s)
+ *  d_ws     at least egat_molecule_attention_workspace_bytes(s): none for short
+ *           molecules, the operands laid out by head for long ones of bf16 (about
+ *           nk * (H dk + D C) * 2 bytes), the parts of a key split for few queries
  *  limits   nq and nk up to 2^30, n_mol up to 2^28
  * Feature and workspace pointers are 16-byte aligned.  Sums and softmax
- * statistics are float32.  Deterministic.  nq = 0 is a no-op.
+ * statistics are float32, and products of float32 storage carry 24 bits (an
+ * infinite float32 value gives NaN where its weight is not zero, too).
+ * Deterministic.  nq = 0 is a no-op.  Molecules of 192 atoms and more on
+ * average, of bf16, run on tcgen05 kernels whose bounded waits report through
+ * egat_take_device_status.
  *
  * egat_molecule_attention_backward: for an upstream gradient G = dL/dm
  * ([nq][D][C] in s->dtype, 16-byte aligned) and the forward's m and lse,

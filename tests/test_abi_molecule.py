@@ -30,7 +30,7 @@ BWD = [OK, OK, OK, OK, OK, OK, OK, OK, OK, OK, OK, OK, 1 << 40, OK, OK, OK, OK, 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(nq=-1), "ARG"), (dict(nk=-1), "ARG"), (dict(n_mol=-1), "ARG"), (dict(cap=-1.0), "ARG"),
-    (dict(cap=float("nan")), "ARG"), (dict(cap=1e-31), "ARG"), (dict(cap=float("inf")), "ARG"), (dict(lmax=4), "UNSUPPORTED"),
+    (dict(cap=float("nan")), "ARG"), (dict(cap=1e-31), "ARG"), (dict(cap=1e31), "ARG"), (dict(cap=float("inf")), "ARG"), (dict(lmax=4), "UNSUPPORTED"),
     (dict(lmax=-1), "UNSUPPORTED"), (dict(C=96), "UNSUPPORTED"), (dict(C=0), "UNSUPPORTED"), (dict(H=3), "UNSUPPORTED"),
     (dict(H=0), "UNSUPPORTED"), (dict(H=32), "UNSUPPORTED"), (dict(dk=12), "UNSUPPORTED"),
     (dict(nq=(1 << 30) + 1), "UNSUPPORTED"), (dict(n_mol=(1 << 28) + 1), "UNSUPPORTED")])

@@ -67,7 +67,7 @@ def test_layouts_on_a_ragged_batch(layout, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("cap", [0.0, 0.5, 20.0, 1e6])
+@pytest.mark.parametrize("cap", [0.0, 0.5, 20.0, 1e6, 1e30])
 @pytest.mark.parametrize("bias,positions", [(False, False), (True, False), (True, True)])
 def test_caps_and_biases(cap, bias, positions, dtype):
     d, g = make(dtype, 2, 128, 16, 16, [130, 65, 3], cap=cap, bias=bias, scale=4.0)
