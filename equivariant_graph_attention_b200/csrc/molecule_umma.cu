@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slot
   const int last = keys ? qk_slices + val_slices : qk_slices;
   if (y > last) return;
   const int row0 = t.row0 + sub * 64, rows = min(64, t.rows - sub * 64);   // may be below one: zeros
-  const int kc = p.dk >> 3, vc = p.ch >> 3, run = p.C >> 3;
+  // logarithms of a run's chunks: a head's part of a query or key, of a degree, a degree
+  const int kc = p.dk >> 3, klog = __ffs(kc) - 1, runlog = __ffs(p.C >> 3) - 1;
   unsigned char* const out = static_cast<unsigned char*>(keys ? p.kv : p.qp);
   const size_t block = keys ? B.key : size_t(B.query) << (mlog - 7), slots = keys ? key_slots : query_slots;
   const size_t in_block = keys ? 0 : size_t(sub >> 1) * B.query + (sub & 1) * 64 * 16;
@@ -98,8 +99,8 @@ __global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slot
   for (int i = threadIdx.x >> 6; i < 16; i += 4) {
     const int x = c0 + i;
     if (x >= chunks) break;
-    const int d = val ? x / run : 0, in = val ? x - d * run : x, per = val ? vc : kc, head = in / per;
-    const int chunk = d * per + in - head * per;
+    const int d = val ? x >> runlog : 0, in = val ? x & ((1 << runlog) - 1) : x, plog = val ? p.ch8log : klog;
+    const int head = in >> plog, chunk = (d << plog) + (in & ((1 << plog) - 1));
     *reinterpret_cast<uint4*>(out + (head * slots + slot) * block + in_block + (val ? B.v : 0) + chunk * chunk_bytes +
                               r * 16) = sm[r][i];
   }
@@ -110,7 +111,7 @@ constexpr int kUmStages = 3;
 // Shared memory of a CTA
 template <int G>
 struct UmLay : UmBlocks {
-  static constexpr int NBARS = 2 * kUmStages + 1 + 6 * G;
+  static constexpr int NBARS = 2 * kUmStages + 2 + 6 * G;
   static constexpr int COLS = 256 * G;   // per group: scores 2 x 64, accumulator up to 128
   int q, pair, bars, slot, flag, total;  // after the stages
   __host__ __device__ UmLay(int dv, int dk) : UmBlocks(dv, dk) {
@@ -133,13 +134,13 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
   const uint32_t base = tc_smem(um), bars = base + L.bars;
   auto full = [&](int s) { return bars + 8 * s; };
   auto freed = [&](int s) { return bars + 8 * (kUmStages + s); };
-  const uint32_t qfull = bars + 8 * 2 * kUmStages;
+  const uint32_t qfull = bars + 8 * 2 * kUmStages, drained = qfull + 8;
   // Two of each by stage parity: a warp may be done with the next stage before
   // another is with this one, and a wait on one barrier for both stages would take
   // the phase before this one for the phase after it.
-  auto sfull = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 1 + 6 * g + b); };
-  auto pready = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 1 + 6 * g + 2 + b); };
-  auto pvdone = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 1 + 6 * g + 4 + b); };
+  auto sfull = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + b); };
+  auto pready = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + 2 + b); };
+  auto pvdone = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + 4 + b); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(um + L.flag);
   const int n = t.o1 - t.o0, stages = (n + kUmStage - 1) / kUmStage;
   const int groups = (t.rows + kUmRows - 1) / kUmRows;   // groups with rows
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
       mbar_init(freed(s), 1);
     }
     mbar_init(qfull, 1);
+    mbar_init(drained, 1);
     for (int g = 0; g < G; ++g) {
       mbar_init(sfull(g, 0), 1);
       mbar_init(sfull(g, 1), 1);
@@ -394,8 +396,8 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
   }
   if (*abort_flag && warp == 8 * G && lane == 0) {   // products in flight end before tensor memory is freed
     volatile int none = 0;
-    um_commit(qfull);   // its second phase: everything issued so far
-    bounded_wait(qfull, 1, kDrainPolls, &none);
+    um_commit(drained);
+    bounded_wait(drained, 0, kDrainPolls, &none);
   }
   um_before();
   __syncthreads();
