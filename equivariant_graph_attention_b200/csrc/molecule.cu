@@ -676,7 +676,7 @@ int by_rows_dk(int dv, int dk, F&& f) {
 // How a pass cuts a shape: rows of a tile and key splits.  Depends on the shape alone.
 struct MolCut {
   bool tc;
-  int umma;     // groups of 128 rows of the tcgen05 kernel, 0: not taken
+  bool umma;    // forward on tcgen05, tiles of 128 rows
   int rwlog;    // log2 of the warps side by side over rows
   int rows;     // rows of a tile
   int groups;   // blocks side by side over heads
@@ -715,13 +715,11 @@ MolCut tile_cut(const egat_mol_shape& s, int n, bool query_gradients = false) {
 }
 MolCut forward_cut(const egat_mol_shape& s) {
   MolCut c = tile_cut(s, s.nq);
-  // Long molecules: tcgen05 tiles of 256 rows, or of 128 where those would leave
-  // SMs idle.
+  // Long molecules: tcgen05 tiles of 128 rows, where a block for every SM remains.
   if (mol_umma_supported(s) && (long long)s.nq >= 192LL * s.n_mol && s.n_mol > 0 && s.nk >= 192LL * s.n_mol) {
-    const long long tiles = tile_blocks(s.nq, s.n_mol, 128, s.H);
-    if (tiles >= 148) {
-      c.umma = tiles >= 8 * 148 ? 2 : 1;
-      c.rows = 128 * c.umma;
+    if (tile_blocks(s.nq, s.n_mol, 128, s.H) >= 148) {
+      c.umma = true;
+      c.rows = 128;
       c.splits = 1;
       return c;
     }
@@ -828,7 +826,7 @@ bool mol_tc_supported(const egat_mol_shape& s) {
 
 size_t molecule_ws_bytes(const egat_mol_shape& s) {
   const MolCut c = forward_cut(s);
-  if (c.umma) return up256(mol_umma_key_bytes(s)) + up256(mol_umma_query_bytes(s, c.umma));
+  if (c.umma) return up256(mol_umma_key_bytes(s)) + up256(mol_umma_query_bytes(s));
   if (c.splits == 1) return 0;
   const size_t rows = size_t(c.splits) * s.nq * s.H;
   return up256(rows * head_columns(s) * sizeof(float)) + up256(rows * 2 * sizeof(float));
@@ -847,8 +845,8 @@ int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d
     p.kv_slots = mol_slots(s.nk, s.n_mol, 64);
     p.kv = d_ws;
     p.qp = static_cast<char*>(d_ws) + up256(mol_umma_key_bytes(s));
-    const int rc = mol_umma_pack(p, c.umma, st);
-    return rc != EGAT_OK ? rc : mol_umma_forward(p, c.umma, st);
+    const int rc = mol_umma_pack(p, st);
+    return rc != EGAT_OK ? rc : mol_umma_forward(p, st);
   }
   if (p.splits > 1) {
     p.part_o = static_cast<float*>(d_ws);

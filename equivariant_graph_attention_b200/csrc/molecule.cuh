@@ -124,12 +124,12 @@ int mol_tc_backward_q_f32(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_k_bf16(const MolParams& p, cudaStream_t st);
 int mol_tc_backward_k_f32(const MolParams& p, cudaStream_t st);
 // tcgen05 kernels: whether they take the shape, the sizes of the operand blocks
-// and their packing, and the forward pass in tiles of 128 * groups rows.
+// and their packing, and the forward pass in tiles of 128 rows.
 bool mol_umma_supported(const egat_mol_shape& s);
 size_t mol_umma_key_bytes(const egat_mol_shape& s);
-size_t mol_umma_query_bytes(const egat_mol_shape& s, int groups);
-int mol_umma_pack(const MolParams& p, int groups, cudaStream_t st);
-int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st);
+size_t mol_umma_query_bytes(const egat_mol_shape& s);
+int mol_umma_pack(const MolParams& p, cudaStream_t st);
+int mol_umma_forward(const MolParams& p, cudaStream_t st);
 
 template <typename K>
 int mol_launch(K* kernel, dim3 grid, int threads, size_t shm, const MolParams& p, cudaStream_t st) {

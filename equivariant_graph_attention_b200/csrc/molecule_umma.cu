@@ -1,21 +1,22 @@
 // Attention within each molecule on the fifth-generation tensor cores: the
 // forward pass over long molecules (bf16 storage).
 //
-// A CTA takes one head and 128 G query rows of a molecule, in G groups of eight
-// warps, and passes over the keys in stages of 64:
+// A CTA takes one head and 128 query rows of a molecule, eight warps of them, and
+// passes over the keys in stages of 64; two CTAs share an SM (one CTA of twice the rows
+// is slower: 2.21 instead of 1.69 ms for 16,384 atoms at lmax 3):
 //  * one warp brings the stages in (bulk copies, one per chunk, three stages in
 //    flight) and writes their positions;
-//  * one thread issues the products: S = Q K^T into one of a group's two
+//  * one thread issues the products: S = Q K^T into one of two
 //    64-column score buffers in tensor memory, and m += P H' with P from tensor
 //    memory, where it replaces the scores;
-//  * a row of a group is two threads', of two warps that share its lanes: each
+//  * a row is two threads', of two warps that share its lanes: each
 //    reads 32 of its 64 scores, applies cap, bias and exponential, and writes its
 //    weights back as bf16.  (One thread with all 64 leaves two warps a scheduler to
 //    hide each other's latency: 0.40 instead of 0.37 ms at 4,096 capped atoms.)  The row's
 //    reference moves only when a score passes it by 2^8; only then do the two
 //    exchange their maxima, and the accumulator is rescaled in place.
-// While a group works on one stage, the tensor core forms its next scores and
-// the other group's products.  Work per pair and head is one exponential (and one
+// While the warps work on one stage, the tensor core forms the next scores and the
+// other CTA's products.  Work per pair and head is one exponential (and one
 // root with a bias) on the special-function unit, which bounds it without a cap
 // (8,191 atoms, lmax 3: 0.24 of 0.48 ms); cap and bias add 13 operations on the FMA
 // pipe and bound it there (4,096 atoms, lmax 2: 0.17 of 0.37 ms).  The products take
@@ -32,7 +33,7 @@ struct UmBlocks {
   int nt, nv;        // value chunks, and to a multiple of 16 columns (the last chunk zeros)
   int ks;            // k-steps of 16 of a score
   int v, pos, key;   // key block: [2 ks chunks][64][16 B], values [nv][64][16 B], x[64], y[64], z[64]
-  int query;         // query block of a group: [2 ks chunks][128][16 B]
+  int query;         // query block: [2 ks chunks][128][16 B]
   __host__ __device__ UmBlocks(int dv, int dk) {
     nt = dv >> 3;
     nv = (nt + 1) & ~1;
@@ -45,23 +46,22 @@ struct UmBlocks {
 };
 
 // q, k, the values and the key positions into those blocks, by head and tile (64
-// keys; groups * 128 query rows): 64 rows and up to 16 chunks a block through shared
+// keys; 128 query rows): 64 rows and up to 16 chunks a block through shared
 // memory, read and written in whole runs.  Rows past a tile are zeros.
-__global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slots, int query_slots, int mlog) {
+__global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slots, int query_slots) {
   const UmBlocks B(p.dv, p.dk);
   __shared__ uint4 sm[64][17];
   const bool keys = int(blockIdx.x) < key_slots;
   const int slot = keys ? blockIdx.x : blockIdx.x - key_slots;
   const MolTile t = keys ? mol_tile(6, p.a.kptr, p.a.kptr, p.nmol, p.nk, p.nk, slot)
-                         : mol_tile(mlog, p.a.qptr, p.a.qptr, p.nmol, p.nq, p.nq, slot);
+                         : mol_tile(kUmRowsLog, p.a.qptr, p.a.qptr, p.nmol, p.nq, p.nq, slot);
   if (t.rows <= 0) return;
   const int qk_chunks = p.H * p.dk / 8, qk_slices = (qk_chunks + 15) / 16;
   const int val_chunks = p.D * p.C / 8, val_slices = (val_chunks + 15) / 16;
   int y = blockIdx.y, sub = 0;
   if (!keys) {   // 64 rows of the tile, slices of q
-    const int subs = 1 << (mlog - 6);
-    sub = y % subs;
-    y /= subs;
+    sub = y & 1;
+    y >>= 1;
   }
   const int last = keys ? qk_slices + val_slices : qk_slices;
   if (y > last) return;
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slot
   // logarithms of a run's chunks: a head's part of a query or key, of a degree, a degree
   const int kc = p.dk >> 3, klog = __ffs(kc) - 1, runlog = __ffs(p.C >> 3) - 1;
   unsigned char* const out = static_cast<unsigned char*>(keys ? p.kv : p.qp);
-  const size_t block = keys ? B.key : size_t(B.query) << (mlog - 7), slots = keys ? key_slots : query_slots;
-  const size_t in_block = keys ? 0 : size_t(sub >> 1) * B.query + (sub & 1) * 64 * 16;
+  const size_t block = keys ? B.key : B.query, slots = keys ? key_slots : query_slots;
+  const size_t in_block = keys ? 0 : sub * 64 * 16;
   const int chunk_bytes = keys ? kUmStage * 16 : kUmRows * 16;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   if (y == last) {   // what no tensor fills, and positions
@@ -107,29 +107,29 @@ __global__ void __launch_bounds__(256) mol_pack_kernel(MolParams p, int key_slot
 }
 
 constexpr int kUmStages = 3;
+constexpr int kUmThreads = 10 * 32;   // eight warps of rows, one of products, one of copies
 
 // Shared memory of a CTA
-template <int G>
 struct UmLay : UmBlocks {
-  static constexpr int NBARS = 2 * kUmStages + 2 + 6 * G;
-  static constexpr int COLS = 256 * G;   // per group: scores 2 x 64, accumulator up to 128
+  static constexpr int NBARS = 2 * kUmStages + 8;
+  static constexpr int COLS = 256;       // tensor memory: scores 2 x 64, accumulator up to 128
   int q, pair, bars, slot, flag, total;  // after the stages
   __host__ __device__ UmLay(int dv, int dk) : UmBlocks(dv, dk) {
     q = kUmStages * key;
-    pair = q + G * query;                  // [4 G pairs of warps][2][32] maxima or sums, then [..][2][2] flags
-    bars = pair + 4 * G * (64 + 4) * 4;
+    pair = q + query;                      // [4 pairs of warps][2][32] maxima or sums, then [..][2][2] flags
+    bars = pair + 4 * (64 + 4) * 4;
     slot = bars + 8 * NBARS;
     flag = slot + 4;
     total = flag + 12;
   }
 };
 
-template <int G, bool CAP, bool BIAS>
-__global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma_kernel(MolParams p) {
-  const UmLay<G> L(p.dv, p.dk);
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p) {
+  const UmLay L(p.dv, p.dk);
   extern __shared__ __align__(128) unsigned char um[];
   const int head = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const MolTile t = mol_tile(G == 2 ? 8 : 7, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
+  const MolTile t = mol_tile(kUmRowsLog, p.a.qptr, p.a.kptr, p.nmol, p.nq, p.nk, blockIdx.x);
   if (t.rows <= 0) return;   // whole CTA
   const uint32_t base = tc_smem(um), bars = base + L.bars;
   auto full = [&](int s) { return bars + 8 * s; };
@@ -138,12 +138,11 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
   // Two of each by stage parity: a warp may be done with the next stage before
   // another is with this one, and a wait on one barrier for both stages would take
   // the phase before this one for the phase after it.
-  auto sfull = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + b); };
-  auto pready = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + 2 + b); };
-  auto pvdone = [&](int g, int b) { return bars + 8 * (2 * kUmStages + 2 + 6 * g + 4 + b); };
+  auto sfull = [&](int b) { return bars + 8 * (2 * kUmStages + 2 + b); };
+  auto pready = [&](int b) { return bars + 8 * (2 * kUmStages + 4 + b); };
+  auto pvdone = [&](int b) { return bars + 8 * (2 * kUmStages + 6 + b); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(um + L.flag);
   const int n = t.o1 - t.o0, stages = (n + kUmStage - 1) / kUmStage;
-  const int groups = (t.rows + kUmRows - 1) / kUmRows;   // groups with rows
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kUmStages; ++s) {
@@ -152,31 +151,28 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
     }
     mbar_init(qfull, 1);
     mbar_init(drained, 1);
-    for (int g = 0; g < G; ++g) {
-      mbar_init(sfull(g, 0), 1);
-      mbar_init(sfull(g, 1), 1);
-      mbar_init(pready(g, 0), 8);
-      mbar_init(pready(g, 1), 8);
-      mbar_init(pvdone(g, 0), 1);
-      mbar_init(pvdone(g, 1), 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(sfull(b), 1);
+      mbar_init(pready(b), 8);
+      mbar_init(pvdone(b), 1);
     }
     mbar_fence_init();
     *abort_flag = 0;
   }
-  if (warp == 8 * G) um_alloc<UmLay<G>::COLS>(base + L.slot);
+  if (warp == 8) um_alloc<UmLay::COLS>(base + L.slot);
   um_before();
   __syncthreads();
   um_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(um + L.slot);
 
-  if (warp == 8 * G + 1) {
+  if (warp == 9) {
     // ---- stages
     const unsigned char* kv = static_cast<const unsigned char*>(p.kv) +
                               (size_t(head) * p.kv_slots + (t.o0 >> 6) + t.seg) * L.key;
     if (lane == 0 && stages > 0) {
-      mbar_arrive_expect_tx(qfull, G * L.query);
-      bulk_g2s(base + L.q, static_cast<const unsigned char*>(p.qp) + (size_t(head) * p.slots + blockIdx.x) * G * L.query,
-               G * L.query, qfull);
+      mbar_arrive_expect_tx(qfull, L.query);
+      bulk_g2s(base + L.q, static_cast<const unsigned char*>(p.qp) + (size_t(head) * p.slots + blockIdx.x) * L.query,
+               L.query, qfull);
       for (int i = 0; i < stages; ++i) {
         const int s = i % kUmStages;
         if (i >= kUmStages && !bounded_wait(freed(s), (i / kUmStages - 1) & 1, kWaitPolls, abort_flag)) break;
@@ -194,54 +190,51 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
         if (last >= 0) bounded_wait(full(s), (last / kUmStages) & 1, kDrainPolls, &none);
       }
     }
-  } else if (warp == 8 * G) {
+  } else if (warp == 8) {
     // ---- products
     if (lane == 0 && stages > 0) {
       bool ok = bounded_wait(qfull, 0, kWaitPolls, abort_flag);
-      auto scores = [&](int i, int g) {
+      auto scores = [&](int i) {
         const uint32_t st = base + (i % kUmStages) * L.key;
 #pragma unroll
         for (int k = 0; k < L.ks; ++k)
-          um_mma_ss(tmem + g * 256 + (i & 1) * kUmStage,
-                    um_k_major<kUmRows>(base + L.q + (g * 2 * L.ks + 2 * k) * kUmRows * 16),
+          um_mma_ss(tmem + (i & 1) * kUmStage,
+                    um_k_major<kUmRows>(base + L.q + 2 * k * kUmRows * 16),
                     um_k_major<kUmStage>(st + 2 * k * kUmStage * 16), um_idesc(kUmStage, false), k > 0);
-        um_commit(sfull(g, i & 1));
+        um_commit(sfull(i & 1));
       };
       ok = ok && bounded_wait(full(0), 0, kWaitPolls, abort_flag);
       um_after();
-      if (ok)
-        for (int g = 0; g < groups; ++g) scores(0, g);
+      if (ok) scores(0);
       for (int i = 0; ok && i < stages; ++i) {
         if (i + 1 < stages) ok = bounded_wait(full((i + 1) % kUmStages), ((i + 1) / kUmStages) & 1, kWaitPolls, abort_flag);
-        for (int g = 0; ok && g < groups; ++g) {
-          // its score buffer holds the weights of stage i - 1 until that product is through
-          if (i > 0) ok = bounded_wait(pvdone(g, (i - 1) & 1), ((i - 1) >> 1) & 1, kWaitPolls, abort_flag);
-          if (!ok) break;
-          um_after();
-          if (i + 1 < stages) scores(i + 1, g);
-          ok = bounded_wait(pready(g, i & 1), (i >> 1) & 1, kWaitPolls, abort_flag);
-          if (!ok) break;
-          um_after();
-          const uint32_t st = base + (i % kUmStages) * L.key;
+        // the next score buffer holds the weights of stage i - 1 until that product is through
+        if (ok && i > 0) ok = bounded_wait(pvdone((i - 1) & 1), ((i - 1) >> 1) & 1, kWaitPolls, abort_flag);
+        if (!ok) break;
+        um_after();
+        if (i + 1 < stages) scores(i + 1);
+        ok = bounded_wait(pready(i & 1), (i >> 1) & 1, kWaitPolls, abort_flag);
+        if (!ok) break;
+        um_after();
+        const uint32_t st = base + (i % kUmStages) * L.key;
 #pragma unroll
-          for (int k = 0; k < kUmStage / 16; ++k)
-            um_mma_ts(tmem + g * 256 + 2 * kUmStage, tmem + g * 256 + (i & 1) * kUmStage + k * 8,
-                      um_mn_major<kUmStage>(st + L.v + k * 256), um_idesc(L.nv * 8, true), i > 0 || k > 0);
-          um_commit(pvdone(g, i & 1));
-        }
-        if (ok) um_commit(freed(i % kUmStages));
+        for (int k = 0; k < kUmStage / 16; ++k)
+          um_mma_ts(tmem + 2 * kUmStage, tmem + (i & 1) * kUmStage + k * 8, um_mn_major<kUmStage>(st + L.v + k * 256),
+                    um_idesc(L.nv * 8, true), i > 0 || k > 0);
+        um_commit(pvdone(i & 1));
+        um_commit(freed(i % kUmStages));
       }
     }
     __syncwarp();
-  } else if ((warp >> 3) < groups) {
+  } else {
     // ---- softmax: a row is two threads'
-    const int g = warp >> 3, half = (warp >> 2) & 1, own = g * kUmRows + (warp & 3) * 32 + lane;
+    const int half = warp >> 2, own = (warp & 3) * 32 + lane;
     const bool live = own < t.rows;
     const size_t row = size_t(t.row0) + (live ? own : 0);
-    const uint32_t tm = tmem + (uint32_t((warp & 3) * 32) << 16) + g * 256;
-    const int pair = g * 4 + (warp & 3);
+    const uint32_t tm = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const int pair = warp & 3;
     volatile float* shared_row = reinterpret_cast<float*>(um + L.pair) + pair * 64 + lane;   // [half] * 32
-    volatile int* flags = reinterpret_cast<int*>(um + L.pair) + 4 * G * 64 + pair * 4;         // [stage & 1][half]
+    volatile int* flags = reinterpret_cast<int*>(um + L.pair) + 4 * 64 + pair * 4;         // [stage & 1][half]
     auto sync_pair = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(1 + pair) : "memory"); };
     f32x2 px = 0, py = 0, pz = 0, slope = 0;
     if (BIAS) {
@@ -259,7 +252,7 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
     // and later waits return at once
     bool ok = true;
     for (int i = 0; i < stages; ++i) {
-      ok = um_wait(sfull(g, i & 1), (i >> 1) & 1, abort_flag) && ok;
+      ok = um_wait(sfull(i & 1), (i >> 1) & 1, abort_flag) && ok;
       if (BIAS) ok = um_wait(full(i % kUmStages), (i / kUmStages) & 1, abort_flag) && ok;   // its positions
       um_after();
       const uint32_t ts = tm + (i & 1) * kUmStage;
@@ -339,7 +332,7 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = f2_add(w[e], shift);
         if (i > 0) {   // rescale the accumulator, once the last stage's product is in it
-          ok = um_wait(pvdone(g, (i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag) && ok;
+          ok = um_wait(pvdone((i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag) && ok;
           um_after();
 #pragma unroll 1
           for (int c = half; c < L.nt; c += 2) {
@@ -369,9 +362,9 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
       um_st_wait();
       um_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pready(g, i & 1));
+      if (lane == 0) mbar_arrive(pready(i & 1));
     }
-    if (ok && stages > 0) ok = um_wait(pvdone(g, (stages - 1) & 1), ((stages - 1) >> 1) & 1, abort_flag);
+    if (ok && stages > 0) ok = um_wait(pvdone((stages - 1) & 1), ((stages - 1) >> 1) & 1, abort_flag);
     um_after();
     float l0, l1;
     f2_unpack(sum, l0, l1);
@@ -394,16 +387,16 @@ __global__ void __launch_bounds__((8 * G + 2) * 32, G == 1 ? 2 : 1) mol_fwd_umma
               make_uint4(tc_pack(v[0], v[1]), tc_pack(v[2], v[3]), tc_pack(v[4], v[5]), tc_pack(v[6], v[7]));
       }
   }
-  if (*abort_flag && warp == 8 * G && lane == 0) {   // products in flight end before tensor memory is freed
+  if (*abort_flag && warp == 8 && lane == 0) {   // products in flight end before tensor memory is freed
     volatile int none = 0;
     um_commit(drained);
     bounded_wait(drained, 0, kDrainPolls, &none);
   }
   um_before();
   __syncthreads();
-  if (warp == 8 * G) {
+  if (warp == 8) {
     um_after();
-    um_dealloc<UmLay<G>::COLS>(tmem);
+    um_dealloc<UmLay::COLS>(tmem);
   }
 }
 
@@ -413,29 +406,27 @@ size_t mol_umma_key_bytes(const egat_mol_shape& s) {
   return size_t(mol_slots(s.nk, s.n_mol, kUmStage)) * s.H *
          UmBlocks((s.lmax + 1) * (s.lmax + 1) * (s.C / s.H), s.dk).key;
 }
-size_t mol_umma_query_bytes(const egat_mol_shape& s, int groups) {
-  return size_t(mol_slots(s.nq, s.n_mol, kUmRows * groups)) * s.H * groups * UmBlocks(8, s.dk).query;
+size_t mol_umma_query_bytes(const egat_mol_shape& s) {
+  return size_t(mol_slots(s.nq, s.n_mol, kUmRows)) * s.H * UmBlocks(8, s.dk).query;
 }
 
-int mol_umma_pack(const MolParams& p, int groups, cudaStream_t st) {
-  const int qk = (p.H * p.dk / 8 + 15) / 16, val = (p.D * p.C / 8 + 15) / 16, subs = 2 * groups;
-  const dim3 grid(p.kv_slots + p.slots, std::max(qk + val + 1, (qk + 1) * subs));
-  mol_pack_kernel<<<grid, 256, 0, st>>>(p, p.kv_slots, p.slots, groups == 2 ? 8 : 7);
+int mol_umma_pack(const MolParams& p, cudaStream_t st) {
+  const int qk = (p.H * p.dk / 8 + 15) / 16, val = (p.D * p.C / 8 + 15) / 16;
+  const dim3 grid(p.kv_slots + p.slots, std::max(qk + val + 1, (qk + 1) * 2));
+  mol_pack_kernel<<<grid, 256, 0, st>>>(p, p.kv_slots, p.slots);
   return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA;
 }
 
-// up to 128 value columns a head: a group's accumulator beside its scores in 256
+// up to 128 value columns a head: the accumulator beside the scores in 256
 // columns of tensor memory
 bool mol_umma_supported(const egat_mol_shape& s) {
   return s.dtype == EGAT_BF16 && (s.lmax + 1) * (s.lmax + 1) * (s.C / s.H) <= 128;
 }
 
-int mol_umma_forward(const MolParams& p, int groups, cudaStream_t st) {
+int mol_umma_forward(const MolParams& p, cudaStream_t st) {
   return mol_flags(p.cap > 0.f, p.a.slope != nullptr, [&](auto cap, auto bias) {
-    constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
-    const dim3 grid(p.slots, p.H);
-    return groups == 2 ? mol_launch(mol_fwd_umma_kernel<2, CAP, BIAS>, grid, 576, UmLay<2>(p.dv, p.dk).total, p, st)
-                       : mol_launch(mol_fwd_umma_kernel<1, CAP, BIAS>, grid, 320, UmLay<1>(p.dv, p.dk).total, p, st);
+    return mol_launch(mol_fwd_umma_kernel<decltype(cap)::value, decltype(bias)::value>, dim3(p.slots, p.H), kUmThreads,
+                      UmLay(p.dv, p.dk).total, p, st);
   });
 }
 

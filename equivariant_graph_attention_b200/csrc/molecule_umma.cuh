@@ -18,8 +18,8 @@
 namespace egat {
 namespace {
 
-constexpr int kUmRows = 128;    // rows of a group (lanes of tensor memory)
-constexpr int kUmStage = 64;    // rows of the other side of a stage
+constexpr int kUmRowsLog = 7, kUmRows = 128;   // rows of a tile (lanes of tensor memory)
+constexpr int kUmStage = 64;                   // rows of the other side of a stage
 
 // Shared-memory matrix descriptor without swizzle (leading and stride byte offsets).
 __device__ __forceinline__ uint64_t um_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {

@@ -1,6 +1,6 @@
-"""GPU tests of the attention within long molecules (the tiles of 128 and 256
-rows with their scores in tensor memory) against the float64 oracle, with the
-bounds of molecule_util: both tile heights, ragged ends, scores that rise along the keys
+"""GPU tests of the attention within long molecules (tiles of 128 rows with
+their scores in tensor memory) against the float64 oracle, with the bounds of
+molecule_util: layouts, ragged ends, scores that rise along the keys
 (the softmax reference moves at every stage), molecules without a finite
 score, NaN of other molecules, graphs and concurrent streams."""
 import numpy as np
