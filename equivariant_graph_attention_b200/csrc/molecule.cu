@@ -685,14 +685,15 @@ struct MolCut {
 long long tile_blocks(int n, int n_mol, int rows, int groups) {
   return ((long long)n / rows + std::min(n_mol, n)) * groups;
 }
-// Tiles of four warps' rows read the other side's rows a quarter as often as tiles
-// of one warp's, whose four warps share those rows instead: taken where `enough`
-// blocks remain and the molecules are that long.
-int wide_log(int n, int n_mol, int rows, int groups, int enough) {
-  int l = 2;
-  while (l > 0 && (tile_blocks(n, n_mol, rows << l, groups) < enough || (long long)n < (long long)(rows / 2 << l) * n_mol))
-    --l;
-  return l;
+// Tiles of four (two) warps' rows read the other side's rows a quarter (half) as often
+// as tiles of one warp's, whose four warps share those rows instead: taken where
+// `four` (`two`) blocks remain and the molecules are that long.
+int wide_log(int n, int n_mol, int rows, int groups, int four, int two) {
+  for (int l = 2; l > 0; --l)
+    if (tile_blocks(n, n_mol, rows << l, groups) >= (l == 2 ? four : two) &&
+        (long long)n >= (long long)(rows / 2 << l) * n_mol)
+      return l;
+  return 0;
 }
 MolCut tile_cut(const egat_mol_shape& s, int n, bool query_gradients = false) {
   MolCut c{};
@@ -700,7 +701,12 @@ MolCut tile_cut(const egat_mol_shape& s, int n, bool query_gradients = false) {
   c.groups = c.tc ? s.H / mol_tc_heads(s, query_gradients) : s.H;
   c.splits = 1;
   if (c.tc) {
-    c.rwlog = wide_log(n, s.n_mol, 16, c.groups, 2 * 148);
+    // 64 rows from 1.2 blocks an SM on, 32 from half a block: at 192 blocks 64 rows are 7 %
+    // faster than 32, at 176 12 % slower, at 128 9 %; at 80 blocks 32 rows are 30 % faster
+    // than 16, whose batches of short molecules take 279 us in place of 124.  Rows of few
+    // value columns cost little to read again: 110 blocks of 32 rows take 55 us, twice as
+    // many of 16 rows 46
+    c.rwlog = wide_log(n, s.n_mol, 16, c.groups, 180, head_columns(s) > 32 ? 74 : 148);
     c.rows = 16 << c.rwlog;
     return c;
   }
@@ -709,15 +715,19 @@ MolCut tile_cut(const egat_mol_shape& s, int n, bool query_gradients = false) {
     w = MolRows<decltype(nv)::value, decltype(lp)::value>::W;
     return 0;
   });
-  c.rwlog = wide_log(n, s.n_mol, w, s.H, 4 * 148);
+  c.rwlog = wide_log(n, s.n_mol, w, s.H, 4 * 148, 4 * 148);
   c.rows = w << c.rwlog;
   return c;
 }
 MolCut forward_cut(const egat_mol_shape& s) {
   MolCut c = tile_cut(s, s.nq);
-  // Long molecules: tcgen05 tiles of 128 rows, where a block for every SM remains.
-  if (mol_umma_supported(s) && (long long)s.nq >= 192LL * s.n_mol && s.n_mol > 0 && s.nk >= 192LL * s.n_mol) {
-    if (tile_blocks(s.nq, s.n_mol, 128, s.H) >= 148) {
+  // Long molecules: tcgen05 tiles of 128 rows, from 512 atoms on, where they fill most of
+  // their last tile, and with 96 blocks.  Both sides measured, bf16 at lmax 2 with a bias:
+  // one system of 500 atoms 24 against 22 us, of 700 27 against 33, of 2,000 75 against
+  // 162; 64 molecules of 200 atoms 119 against 85, of 400 273 against 240; 56 blocks of
+  // 8-column heads 74 against 44.
+  if (mol_umma_supported(s) && s.n_mol > 0 && (long long)s.nq >= 512LL * s.n_mol && (long long)s.nk >= 512LL * s.n_mol) {
+    if (tile_blocks(s.nq, s.n_mol, 128, s.H) >= 96) {
       c.umma = true;
       c.rows = 128;
       c.splits = 1;

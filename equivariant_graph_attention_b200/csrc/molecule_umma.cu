@@ -18,8 +18,8 @@
 // While the warps work on one stage, the tensor core forms the next scores and the
 // other CTA's products.  Work per pair and head is one exponential (and one
 // root with a bias) on the special-function unit, which bounds it without a cap
-// (8,191 atoms, lmax 3: 0.24 of 0.48 ms); cap and bias add 13 operations on the FMA
-// pipe and bound it there (4,096 atoms, lmax 2: 0.17 of 0.37 ms).  The products take
+// (8,191 atoms, lmax 3: 0.24 of 0.46 ms); cap and bias add 13 operations on the FMA
+// pipe and bound it there (4,096 atoms, lmax 2: 0.17 of 0.35 ms).  The products take
 // about a third of the exponentials' time at 16 + 72 columns.  Every wait is bounded.
 #include <algorithm>
 

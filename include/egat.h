@@ -423,7 +423,7 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  * Feature and workspace pointers are 16-byte aligned.  Sums and softmax
  * statistics are float32, and products of float32 storage carry 24 bits (an
  * infinite float32 value gives NaN where its weight is not zero, too).
- * Deterministic.  nq = 0 is a no-op.  Molecules of 192 atoms and more on
+ * Deterministic.  nq = 0 is a no-op.  Molecules of 512 atoms and more on
  * average, of bf16, run on tcgen05 kernels whose bounded waits report through
  * egat_take_device_status.
  *

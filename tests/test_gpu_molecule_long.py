@@ -45,6 +45,7 @@ def _check(d, g=None, dtype="bf16", positions=True):
     ((2, 128, 16, 16), [1300, 257, 700]), ((3, 128, 16, 16), [600, 901]), ((2, 64, 8, 16), [1500, 900]),
     ((1, 128, 8, 32), [1501, 905]), ((1, 32, 4, 8), [300] * 20), ((0, 16, 2, 8), [201] * 45),
     ((2, 128, 16, 16), [300] * 24), ((3, 128, 16, 16), [193, 400, 257] * 9), ((1, 32, 4, 8), [1000, 0, 1] + [700] * 45),
+    ((0, 16, 2, 8), [700] * 10), ((0, 64, 4, 16), [1100] * 5), ((2, 64, 8, 8), [640, 700, 513]),
 ], ids=str)
 @pytest.mark.parametrize("cap", [0.0, 3.0])
 def test_layouts(layout, lengths, cap):
@@ -61,7 +62,7 @@ def test_caps_and_biases(cap, bias, positions):
     _check(d, g, positions=positions)
 
 
-@pytest.mark.parametrize("queries,keys", [([1300, 700], [200, 900]), ([1200, 900], [0, 800]), ([2100], [449])], ids=str)
+@pytest.mark.parametrize("queries,keys", [([1300, 700], [200, 900]), ([1200, 900], [0, 800]), ([2100], [449]), ([1200, 900], [0, 1100]), ([600, 1500], [513, 512])], ids=str)
 def test_other_keys(queries, keys):
     d, g = make("bf16", 2, 128, 16, 16, keys, queries=queries, cap=5.0, behind=2)
     _check(d, g)
@@ -81,8 +82,9 @@ def test_scores_that_rise_along_the_keys(lengths, cap):
         _check(d, g if len(lengths) < 4 else None)
 
 
-def test_nan_stays_in_its_molecule():
-    d, _ = make("bf16", 2, 128, 16, 16, [400, 700, 333], front=1, behind=4)
+@pytest.mark.parametrize("lengths", [[400, 700, 333], [640, 701, 577]], ids=str)
+def test_nan_stays_in_its_molecule(lengths):
+    d, _ = make("bf16", 2, 128, 16, 16, lengths, front=1, behind=4)
     _, (m, lse) = _forward(d)
     a, b = d["q_ptr"][1], d["q_ptr"][2]
     for n in ("k", "hp", "pos_q"):
@@ -95,8 +97,9 @@ def test_nan_stays_in_its_molecule():
     assert torch.isnan(m2[a:b]).any()
 
 
-def test_keys_at_infinite_distance_have_no_weight():
-    d, _ = make("bf16", 2, 128, 16, 16, [449], queries=[2100])
+@pytest.mark.parametrize("keys", [449, 577])
+def test_keys_at_infinite_distance_have_no_weight(keys):
+    d, _ = make("bf16", 2, 128, 16, 16, [keys], queries=[2100])
     d["slope"] = np.abs(d["slope"])
     d["pos_k"][:130] = 3e38                 # the first stages have no finite score
     d["pos_k"][200::9] = 3e38
