@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_q_kernel(MolParams p) {
           const float4 r = *reinterpret_cast<const float4*>(sp + 4 * j);
           dx = rx - r.x, dy = ry - r.y, dz = rz - r.z;
           d = mol_sqrt(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+          if (d == INFINITY) dx = mol_finite(dx), dy = mol_finite(dy), dz = mol_finite(dz);
         }
         const float w = pair_weight(p, x, slope * kLog2e * d, lse2, slope_x);
         if (sweep == 0) {
@@ -529,6 +530,7 @@ __global__ void __launch_bounds__(kMolThreads) mol_bwd_k_kernel(MolParams p) {
         const float4 r = *reinterpret_cast<const float4*>(sp + 4 * j);
         dx = rx - r.x, dy = ry - r.y, dz = rz - r.z;
         d = mol_sqrt(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        if (d == INFINITY) dx = mol_finite(dx), dy = mol_finite(dy), dz = mol_finite(dz);
       }
       const float w = pair_weight(p, x, slope * kLog2e * d, sl[2 * j], slope_x);
       const float ds = w * (dp - sl[2 * j + 1]);

@@ -113,6 +113,10 @@ __device__ __forceinline__ float mol_sqrt(float x) {
   return r;
 }
 
+// An infinite distance masks its pair, whose position gradient is then zero times
+// the direction: a direction of infinite components would make that NaN.
+__device__ __forceinline__ float mol_finite(float x) { return copysignf(fminf(fabsf(x), 3.4e38f), x); }
+
 // Tensor-core kernels in tiles of 16 << p.rwlog rows: whether they take the shape,
 // the heads that a warp takes together, and their launches.
 bool mol_tc_supported(const egat_mol_shape& s);

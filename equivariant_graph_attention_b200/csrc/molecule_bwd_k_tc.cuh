@@ -174,16 +174,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
           tc_apply<KC, DP>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK);
         }
         if (POS) {
+          const bool far = tc_far(d);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const f32x2 dir[3] = {f2_add(at[0], px[r]), f2_add(at[kTcStage / 2], py[r]), f2_add(at[kTcStage], pz[r])};
-              const f32x2 f = f2_mul(u[c][r], ri[c][r]);
-#pragma unroll
-              for (int e = 0; e < 3; ++e) gs[r][e] = f2_fma(f, dir[e], gs[r][e]);
-            }
+            for (int r = 0; r < 2; ++r)
+              tc_pull(far, reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2), px[r], py[r], pz[r],
+                      f2_mul(u[c][r], ri[c][r]), gs[r]);
           }
         }
       }

@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
         f32x2 d[2][2] = {}, ri[2][2] = {};   // distances (and their reciprocals): [8-key tile][row]
         if constexpr (BIAS) tc_dists<POS>(sp + j + t2, px, py, pz, d, ri);
         f32x2 u[2][2] = {}, dc[2][2] = {};   // POS: sum over the heads of slope dS; finite distances
+        bool far = false;
         if constexpr (POS) {
+          far = tc_far(d);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a, b;   // a distance may be inf where the weight is zero
@@ -205,11 +207,8 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
               u[c][r] = f2_fma(ds, slope[h], u[c][r]);
               sd[h][r] = f2_fma(ds, dc[c][r], sd[h][r]);
               if (FIX) {
-                const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
-                const f32x2 wr = f2_mul(w, ri[c][r]);
-                ga[h][r][0] = f2_fma(wr, f2_add(at[0], px[r]), ga[h][r][0]);
-                ga[h][r][1] = f2_fma(wr, f2_add(at[kTcStage / 2], py[r]), ga[h][r][1]);
-                ga[h][r][2] = f2_fma(wr, f2_add(at[kTcStage], pz[r]), ga[h][r][2]);
+                tc_pull(far, reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2), px[r], py[r], pz[r], f2_mul(w, ri[c][r]),
+                        ga[h][r]);
                 sa[h][r] = f2_fma(w, dc[c][r], sa[h][r]);
               }
             }
@@ -229,14 +228,10 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
         if constexpr (POS) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const f32x2* at = reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const f32x2 f = f2_mul(u[c][r], ri[c][r]);
-              gs[r][0] = f2_fma(f, f2_add(at[0], px[r]), gs[r][0]);
-              gs[r][1] = f2_fma(f, f2_add(at[kTcStage / 2], py[r]), gs[r][1]);
-              gs[r][2] = f2_fma(f, f2_add(at[kTcStage], pz[r]), gs[r][2]);
-            }
+            for (int r = 0; r < 2; ++r)
+              tc_pull(far, reinterpret_cast<const f32x2*>(sp + j + 8 * c + t2), px[r], py[r], pz[r],
+                      f2_mul(u[c][r], ri[c][r]), gs[r]);
           }
         }
       }

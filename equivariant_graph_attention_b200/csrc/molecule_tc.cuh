@@ -597,6 +597,39 @@ __device__ __forceinline__ void tc_dists(const float* sp, const f32x2 (&px)[2], 
   }
 }
 
+// Whether any distance of a warp's step is infinite
+__device__ __forceinline__ bool tc_far(const f32x2 (&d)[2][2]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_unpack(d[i >> 1][i & 1], a, b);
+    top = tc_max3(top, a, b);
+  }
+  return __any_sync(~0u, top == INFINITY);
+}
+// g += f (r_j - r_i) by component; FAR: a direction may be infinite, where f is zero
+template <bool FAR>
+__device__ __forceinline__ void tc_pull(const f32x2* at, f32x2 px, f32x2 py, f32x2 pz, f32x2 f, f32x2 (&g)[3]) {
+  f32x2 v[3] = {f2_add(at[0], px), f2_add(at[kTcStage / 2], py), f2_add(at[kTcStage], pz)};
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    if (FAR) {
+      float a, b;
+      f2_unpack(v[e], a, b);
+      v[e] = f2_pack(mol_finite(a), mol_finite(b));
+    }
+    g[e] = f2_fma(f, v[e], g[e]);
+  }
+}
+// ... by a flag that is the same for the whole warp and nearly always false
+__device__ __forceinline__ void tc_pull(bool far, const f32x2* at, f32x2 px, f32x2 py, f32x2 pz, f32x2 f, f32x2 (&g)[3]) {
+  if (__builtin_expect(far, 0))
+    tc_pull<true>(at, px, py, pz, f, g);
+  else
+    tc_pull<false>(at, px, py, pz, f, g);
+}
+
 // Calls f with the value tiles, the query chunks and the heads of a warp: two for up
 // to 64 value columns, HP9 for 72, and one where the registers would not hold two.
 template <int PL, int HP9, typename F>

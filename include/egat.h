@@ -405,7 +405,11 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  * joined.  A row of no molecule (before the first or behind the last) and a
  * row whose molecule has no keys get m = 0 and lse = -inf; rows of other
  * molecules never reach a row's result, not even as NaN.  A score of -inf (an
- * infinite distance) masks its pair; a row of nothing else is an empty row.
+ * infinite distance, times a slope above zero) masks its pair: no weight, and
+ * zeros in every gradient.  Its h' row still meets a weight of zero, so it has
+ * to be finite.  A row of nothing else is an empty row.  (In the self form a row
+ * at infinity has no distance to itself and is NaN: infinite coordinates are for
+ * d_pos_k, or queries of the other form.)
  *  s->lmax  0..3 (0: plain scalar values), C, H, dk as in the module header;
  *           lmax, C and H split the values by head as in step 3
  *  s->cap   0 = no cap; from 1e-30 to 1e30 otherwise
