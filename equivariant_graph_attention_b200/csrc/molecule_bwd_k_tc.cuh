@@ -8,7 +8,7 @@ namespace egat {
 namespace {
 
 // Bound by latency at two blocks an SM: the accumulators and the key rows' fragments
-// fill the registers (4,096 atoms capped: 0.65 ms, a third of the tensor pipe and of
+// fill the registers (4,096 atoms capped: 0.73 ms, a third of the tensor pipe and of
 // the issue slots).
 //
 // dL/dk, dL/dh' and, with POS, the key side of dL/dr: a warp owns 16 key rows
@@ -22,6 +22,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
   // planes of dS: its terms cancel in the sum, and two planes of bf16 storage take the
   // rounding of one out of it (1.6 times the error of the result's own rounding)
   constexpr int DP = PL == 1 ? 2 : 3;
+  // planes of the weights: as many, or dh' would hold each one's rounding beside its own
+  // (4,096 atoms capped: 0.63 ms with one)
+  constexpr int WP = DP;
   // the key rows' values as A fragments: in registers, or read again for every
   // step where they would not fit beside the accumulators
   constexpr bool VREG = NT * PL <= 27;
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
             for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], c_in);
             tc_cap<4, true>(x, fx);
           }
-          uint32_t fd[DP][2][2], fa[PL][2][2];
+          uint32_t fd[DP][2][2], fa[WP][2][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = i >> 1, r = i & 1;
@@ -163,14 +166,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) mol_bwd_k_tc_kernel(MolParams p
             f2_unpack(x[i], a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
-            tc_put<PL>(fa, c, r, a, b);
+            tc_put<WP>(fa, c, r, a, b);
             f32x2 ds = f2_mul(f2_pack(a, b), f2_add(f2_pack(dp[c][2 * r], dp[c][2 * r + 1]), row[kTcStage / 2]));
             if (POS) u[c][r] = f2_fma(ds, slope[h], u[c][r]);
             if constexpr (CAP) ds = f2_mul(ds, fx[i]);
             f2_unpack(ds, a, b);
             tc_put<DP>(fd, c, r, a, b);
           }
-          tc_apply<NT, PL>(dv[h], fa, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV);
+          tc_apply<NT, WP>(dv[h], fa, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16, L::PV);
           tc_apply<KC, DP>(dk[h], fd, st + L::QK + j * L::RK + h * KC * 16 + tc_lane_t(L::RK, 16), 16, L::PK);
         }
         if (POS) {

@@ -7,14 +7,16 @@ namespace egat {
 namespace {
 
 // Short molecules, few rows and float32.  Bound by latency: three blocks of four warps
-// an SM keep 45 % of the issue slots busy (512 molecules of 5 to 120 atoms: 124 us, of
-// which the memory traffic is 27).  Four blocks an SM spill or take one head a warp, two
-// hide less (142 to 162 us); blocks that take several head groups in turn are fewer and
-// end less evenly (138 us).
+// an SM keep 45 % of the issue slots busy (512 molecules of 5 to 120 atoms: 137 us, of
+// which the memory traffic is 27).  With one plane of the weights, at 124 us: four blocks an
+// SM spill or take one head a warp, two hide less (142 to 162 us); blocks that take several
+// head groups in turn are fewer and end less evenly (138 us).
 //
 // Per 16 x 16 pairs and head: S = Q K^T (one k-step of 16, two at dk 32), base-2
-// scores in packed float32 pairs, the online softmax, and m += P H' with P
-// rounded once to bf16 (bf16 storage; the normaliser adds the unrounded weights).  A row's
+// scores in packed float32 pairs, the online softmax, and m += P H' with P as the
+// sum of two bf16 numbers (bf16 storage; the normaliser adds the unrounded weights): with
+// one, m was off by up to 1.4 times its own rounding (0.0023 of it in place of 0.0017), for
+// 124 us in place of 137 at 512 molecules, 39 in place of 41 for one row against 32,768.  A row's
 // reference moves only when a score passes it by 2^8, so most steps need no
 // exchange between lanes and no rescaling; the rare step that moves it works its
 // scores out again, which keeps them out of the registers in between.
@@ -22,6 +24,7 @@ template <int NT, int KC, int HP, int PL, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kernel(MolParams p) {
   using L = TcLay<NT, KC, HP, PL>;
   using T = typename L::T;
+  constexpr int WP = PL == 1 ? 2 : 3;   // planes of the weights
   extern __shared__ __align__(128) unsigned char tsm[];
   const int head0 = blockIdx.y * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
         first = false;
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          uint32_t pf[PL][2][2];
+          uint32_t pf[WP][2][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a, b;
@@ -200,9 +203,9 @@ __global__ void __launch_bounds__(kTcThreads, NT <= 18 ? 3 : 2) mol_fwd_tc_kerne
             a = fast_exp2(a);
             b = fast_exp2(b);
             sum[h][i & 1] = f2_add(sum[h][i & 1], f2_pack(a, b));
-            tc_put<PL>(pf, i >> 1, i & 1, a, b);
+            tc_put<WP>(pf, i >> 1, i & 1, a, b);
           }
-          tc_apply<NT, PL>(acc[h], pf, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16,
+          tc_apply<NT, WP>(acc[h], pf, st + L::VAL + j * L::RV + h * 16 + tc_lane_t(L::RV, HP * 16), HP * 16,
                            L::PV);
         }
       }

@@ -11,16 +11,19 @@
 //    memory, where it replaces the scores;
 //  * a row is two threads', of two warps that share its lanes: each
 //    reads 32 of its 64 scores, applies cap, bias and exponential, and writes its
-//    weights back as bf16.  (One thread with all 64 leaves two warps a scheduler to
+//    weights back as the sum of two bf16 numbers, one behind the other over the 64
+//    columns of the scores.  (One thread with all 64 leaves two warps a scheduler to
 //    hide each other's latency: 0.40 instead of 0.37 ms at 4,096 capped atoms.)  The row's
 //    reference moves only when a score passes it by 2^8; only then do the two
 //    exchange their maxima, and the accumulator is rescaled in place.
 // While the warps work on one stage, the tensor core forms the next scores and the
 // other CTA's products.  Work per pair and head is one exponential (and one
-// root with a bias) on the special-function unit, which bounds it without a cap
-// (8,191 atoms, lmax 3: 0.24 of 0.46 ms); cap and bias add 13 operations on the FMA
-// pipe and bound it there (4,096 atoms, lmax 2: 0.17 of 0.35 ms).  The products take
-// about a third of the exponentials' time at 16 + 72 columns.  Every wait is bounded.
+// root with a bias) on the special-function unit (8,191 atoms, lmax 3: 0.24 of 0.64 ms);
+// cap and bias add 13 operations on the FMA pipe and bound it there (4,096 atoms, lmax 2:
+// 0.17 of 0.37 ms).  The products take two thirds of the exponentials' time at 72 value
+// columns and as much as they at 128 (16 + 2 x 128 columns a pair: 0.33 ms at the measured
+// rate), where they bound it.  One plane of the weights took 0.35 and 0.46 ms for these
+// two, with an error of m up to 1.4 times that of its own rounding.  Every wait is bounded.
 #include <algorithm>
 
 #include "molecule_umma.cuh"
@@ -219,8 +222,9 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
         const uint32_t st = base + (i % kUmStages) * L.key;
 #pragma unroll
         for (int k = 0; k < kUmStage / 16; ++k)
-          um_mma_ts(tmem + 2 * kUmStage, tmem + (i & 1) * kUmStage + k * 8, um_mn_major<kUmStage>(st + L.v + k * 256),
-                    um_idesc(L.nv * 8, true), i > 0 || k > 0);
+          for (int w = 0; w < 2; ++w)   // the weights' planes
+            um_mma_ts(tmem + 2 * kUmStage, tmem + (i & 1) * kUmStage + w * 32 + k * 8,
+                      um_mn_major<kUmStage>(st + L.v + k * 256), um_idesc(L.nv * 8, true), i > 0 || k > 0 || w > 0);
         um_commit(pvdone(i & 1));
         um_commit(freed(i % kUmStages));
       }
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
         }
         break;
       }
-      uint32_t pk[16];
+      uint32_t pk[2][16];   // the weights as the sum of two bf16 numbers
       f32x2 part[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -355,10 +359,14 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
         a = fast_exp2(a);
         b = fast_exp2(b);
         part[e & 1] = f2_add(part[e & 1], f2_pack(a, b));
-        pk[e] = tc_pack(a, b);
+        uint32_t w2[2];
+        tc_planes<2>(a, b, w2);
+        pk[0][e] = w2[0];
+        pk[1][e] = w2[1];
       }
       sum = f2_add(sum, f2_add(part[0], part[1]));
-      um_st16(ts + half * 16, pk);
+      um_st16(ts + half * 16, pk[0]);
+      um_st16(ts + 32 + half * 16, pk[1]);
       um_st_wait();
       um_before();
       __syncwarp();

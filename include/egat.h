@@ -417,7 +417,8 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  *  d_pos_q, d_pos_k float32 [nq][3], [nk][3]; d_slope float32 [H], any sign:
  *           all used if d_slope is not NULL, none otherwise
  *  d_m      [nq][D][C] in s->dtype (bf16 storage: the softmax weights enter
- *           the value products as bf16, so a wider result would not hold more)
+ *           the value products to 2^-16 of themselves, as the sum of two bf16
+ *           numbers, here and in dL/dh'; the result is rounded once)
  *  d_lse    float32 [nq][H], natural logarithm; may be NULL (the backward
  *           pass needs it)
  *  d_ws     at least egat_molecule_attention_workspace_bytes(s): none for short
