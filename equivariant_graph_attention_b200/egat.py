@@ -8,6 +8,11 @@ fallback: importing the library fails loudly when ``libegat.so`` is missing
 (build it with ``python -m equivariant_graph_attention_b200.build``).
 
 Function names match the C entry points (``egat_build_graph`` ...).
+
+``stream`` is the torch stream that a call runs on, the current one by default.
+A call allocates its results and workspace on that stream, and keeps inputs and
+results allocated while a stream uses them.  The caller orders the stream behind
+whatever writes the inputs, and other streams behind it before they read the results.
 """
 from __future__ import annotations
 
@@ -556,17 +561,33 @@ def _elsewhere(dev: int) -> bool:
     return torch._C._cuda_getDevice() != dev
 
 
-def _stream_of(stream, dev: int) -> int:
-    """The given stream, or the device's current one, as an integer handle."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _stream_of(dev: int) -> int:
+    """The device's current stream as an integer handle."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _used_on(stream, *tensors) -> None:
-    """Memory that a call allocated on the current stream is also in use on the stream it was given."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _tensors(*values):
+    """The CUDA tensors among these values."""
+    return [t for t in values if isinstance(t, torch.Tensor) and t.is_cuda]
+
+
+def _moved(f, dev: int, stream, *args):
+    """f(*args) with the tensors' device and the given stream current.  What the call allocates is then
+    that stream's own memory: a block that the caller's stream has given back but may still write is not
+    among it.  Inputs stay allocated until the stream is done with them, results until the caller's stream is."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            return f(*args)
+        if stream.device.index != dev:
+            raise ValueError(f"egat: the stream must belong to CUDA device {dev}, not to {stream.device}")
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = f(*args)
+    for t in _tensors(*args):
+        t.record_stream(stream)
+    for t in _tensors(*out):
+        t.record_stream(here)
+    return out
 
 
 def _scratch(nb: int, workspace: Optional[torch.Tensor], like: torch.Tensor):
@@ -619,10 +640,9 @@ def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tens
     device; k_ptr None: the queries' own atoms).  Returns (m [nq, D, C] in the storage type,
     lse float32 [nq, H] or None); rows without keys get 0 and -inf."""
     dev = _device(q)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return egat_molecule_attention(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, want_lse, out,
-                                           workspace, stream)
+    if stream is not None or _elsewhere(dev):
+        return _moved(egat_molecule_attention, dev, stream, shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, want_lse,
+                      out, workspace)
     ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
     cs, nb, _ = _mol_call(shape)
     vals = (shape.nq, shape.D, shape.C)
@@ -634,9 +654,8 @@ def egat_molecule_attention(shape: MoleculeShape, q: torch.Tensor, k: torch.Tens
     lse = torch.empty((shape.nq, shape.H), dtype=torch.float32, device=q.device) if want_lse else None
     ws, nb = _scratch(nb, workspace, q)
     rc = load_library().egat_molecule_attention(cs, *ptrs, None if ws is None else ws.data_ptr(), nb, po,
-                                                None if lse is None else lse.data_ptr(), _stream_of(stream, dev))
+                                                None if lse is None else lse.data_ptr(), _stream_of(dev))
     _check("egat_molecule_attention", rc)
-    _used_on(stream, out, lse, ws)
     return out, lse
 
 
@@ -657,10 +676,9 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
     whole dL/dr and dpos_k is None; without a slope, or with positions=False (cheaper), the
     last three are None."""
     dev, T = _device(q), shape.torch_dtype
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return egat_molecule_attention_backward(shape, q, k, hp, q_ptr, m, lse, grad_m, k_ptr, pos_q, pos_k, slope,
-                                                    positions, workspace, stream)
+    if stream is not None or _elsewhere(dev):
+        return _moved(egat_molecule_attention_backward, dev, stream, shape, q, k, hp, q_ptr, m, lse, grad_m, k_ptr, pos_q,
+                      pos_k, slope, positions, workspace)
     ptrs = _mol_inputs(shape, q, k, hp, q_ptr, k_ptr, pos_q, pos_k, slope, dev)
     cs, _, nb = _mol_call(shape)
     vals = (shape.nq, shape.D, shape.C)
@@ -674,9 +692,8 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
         dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
     at = [None if t is None else t.data_ptr() for t in (ws, dq, dk, dhp, dpos_q, dpos_k, dslope)]
     rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
-                                                         _stream_of(stream, dev))
+                                                         _stream_of(dev))
     _check("egat_molecule_attention_backward", rc)
-    _used_on(stream, ws, dq, dk, dhp, dpos_q, dpos_k, dslope)
     return dq, dk, dhp, dpos_q, dpos_k, dslope
 
 
@@ -710,9 +727,8 @@ def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     works in place), weight and bias float32 [width].  Returns (y, stats float32 [n, 2] = mean
     and 1/std, or None).  out may be x itself."""
     dt, dev, shape, T = _norm_dtype(x), _device(x), x.shape, x.dtype
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return egat_layer_norm(x, weight, bias, eps, want_stats, out, stream)
+    if stream is not None or _elsewhere(dev):
+        return _moved(egat_layer_norm, dev, stream, x, weight, bias, eps, want_stats, out)
     n, width = shape
     px, ldx = _norm_rows("x", x, T, shape, dev)
     pw = _typed("weight", weight, torch.float32, (width,), dev)
@@ -724,9 +740,8 @@ def egat_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         py, ldy = _norm_rows("out", out, T, shape, dev)
     stats = torch.empty((n, 2), dtype=torch.float32, device=x.device) if want_stats else None
     rc = load_library().egat_layer_norm(px, ldx, n, width, dt, pw, pb, eps, py, ldy,
-                                        None if stats is None else stats.data_ptr(), _stream_of(stream, dev))
+                                        None if stats is None else stats.data_ptr(), _stream_of(dev))
     _check("egat_layer_norm", rc)
-    _used_on(stream, out, stats)
     return out, stats
 
 
@@ -748,9 +763,8 @@ def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], st
     """(dx in x's type, dweight, dbias float32 [width]) of the layer norm for the upstream
     gradient grad_y; stats as returned by the forward.  out (any row stride) receives dx."""
     dt, dev, shape, T = _norm_dtype(x), _device(x), x.shape, x.dtype
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return egat_layer_norm_backward(x, weight, stats, grad_y, out, workspace, stream)
+    if stream is not None or _elsewhere(dev):
+        return _moved(egat_layer_norm_backward, dev, stream, x, weight, stats, grad_y, out, workspace)
     n, width = shape
     px, ldx = _norm_rows("x", x, T, shape, dev)
     pg, ldg = _norm_rows("grad_y", grad_y, T, shape, dev)
@@ -765,7 +779,6 @@ def egat_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], st
     ws, nb = _scratch(_norm_ws(n, width), workspace, x)
     rc = load_library().egat_layer_norm_backward(px, ldx, n, width, dt, pw, ps, pg, ldg,
                                                  None if ws is None else ws.data_ptr(), nb, po, ldo,
-                                                 dw.data_ptr(), db.data_ptr(), _stream_of(stream, dev))
+                                                 dw.data_ptr(), db.data_ptr(), _stream_of(dev))
     _check("egat_layer_norm_backward", rc)
-    _used_on(stream, out, dw, db, ws)
     return out, dw, db
