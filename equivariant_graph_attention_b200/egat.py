@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -177,6 +178,54 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _tensors(*values):
+    """The CUDA tensors among these values and in the containers among them."""
+    out = []
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            out += [v] if v.is_cuda else []
+        elif isinstance(v, (tuple, list)):
+            out += _tensors(*v)
+        elif isinstance(v, dict):
+            out += _tensors(*v.values())
+    return out
+
+
+def _moved(f, dev: int, stream, *args, **kw):
+    """f(*args) with the tensors' device and the given stream current.  What the call allocates is then
+    that stream's own memory: a block that the caller's stream has given back but may still write is not
+    among it.  Inputs stay allocated until the stream is done with them, results until the caller's stream is."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            return f(*args, **kw)
+        if stream.device.index != dev:
+            raise ValueError(f"egat: the stream must belong to CUDA device {dev}, not to {stream.device}")
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = f(*args, **kw)
+    for t in _tensors(args, kw):
+        t.record_stream(stream)
+    for t in _tensors(out):
+        t.record_stream(here)
+    return out
+
+
+def _on_stream(f):
+    """f as it is on the current stream; with a stream, through _moved."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        kw.pop("stream", None)
+        args = args[:at] + args[at + 1:]
+        at_hand = _tensors(args, kw)
+        return _moved(f, at_hand[0].device.index if at_hand else stream.device.index, stream, *args, **kw)
+    return call
+
+
 @dataclass(frozen=True)
 class Shape:
     n: int
@@ -235,6 +284,7 @@ def egat_forward_workspace_bytes(shape: Shape) -> int:
     return out.value
 
 
+@_on_stream
 def egat_build_graph(pos_q: torch.Tensor, cutoff_q: int, K: int = 0, mode: str = "padded",
                      col_capacity: int = 0, want_order: bool = True,
                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
@@ -275,6 +325,7 @@ def egat_build_graph(pos_q: torch.Tensor, cutoff_q: int, K: int = 0, mode: str =
     return out
 
 
+@_on_stream
 def egat_eaas_couple(shape: Shape, x: torch.Tensor, pos: torch.Tensor, w: torch.Tensor,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """EAAS coupling y = x (x) R(pos) with path weights w [P, C]; x, y [n, D, C]."""
@@ -287,6 +338,7 @@ def egat_eaas_couple(shape: Shape, x: torch.Tensor, pos: torch.Tensor, w: torch.
     return out
 
 
+@_on_stream
 def egat_qk_projection(shape: Shape, h: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
                        q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
                        stream=None):
@@ -309,6 +361,7 @@ def egat_escn_num_weights(lmax: int, mmax: int) -> int:
     return load_library().egat_escn_num_weights(lmax, mmax)
 
 
+@_on_stream
 def egat_escn_conv(shape: Shape, mmax: int, h: torch.Tensor, pos: torch.Tensor, nbr: torch.Tensor,
                    cnt: Optional[torch.Tensor], w: torch.Tensor, order: Optional[torch.Tensor] = None,
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -324,6 +377,7 @@ def egat_escn_conv(shape: Shape, mmax: int, h: torch.Tensor, pos: torch.Tensor, 
     return out
 
 
+@_on_stream
 def egat_otf_attention(shape: Shape, q: torch.Tensor, k: torch.Tensor, hp: torch.Tensor,
                        nbr_or_rowptr: torch.Tensor, cnt_or_col: Optional[torch.Tensor],
                        order: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -339,6 +393,7 @@ def egat_otf_attention(shape: Shape, q: torch.Tensor, k: torch.Tensor, hp: torch
     return out
 
 
+@_on_stream
 def egat_otf_attention_coupled(shape: Shape, q: torch.Tensor, k: torch.Tensor, hp: torch.Tensor,
                                nbr_or_rowptr: torch.Tensor, cnt_or_col: Optional[torch.Tensor],
                                pos: torch.Tensor, w2: torch.Tensor,
@@ -363,6 +418,7 @@ def egat_attention_plan_bytes(shape: Shape) -> int:
     return out.value
 
 
+@_on_stream
 def egat_build_attention_plan(shape: Shape, nbr: torch.Tensor, cnt: Optional[torch.Tensor],
                               order: Optional[torch.Tensor] = None,
                               pos: Optional[torch.Tensor] = None,
@@ -389,6 +445,7 @@ def egat_backward_workspace_bytes(shape: Shape) -> int:
     return out.value
 
 
+@_on_stream
 def egat_backward(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: torch.Tensor,
                   k: torch.Tensor, nbr: torch.Tensor, cnt: Optional[torch.Tensor],
                   w1: torch.Tensor, w2: torch.Tensor, grad_out: torch.Tensor,
@@ -415,6 +472,7 @@ def egat_backward(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: torch.Ten
     return dh, dq, dk, dpos
 
 
+@_on_stream
 def egat_gather_rows(src: torch.Tensor, idx: torch.Tensor, out: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """out[r] = src[idx[r]] along the first dimension (an index outside
@@ -441,6 +499,7 @@ def egat_selftest_wait_timeout(polls: int = 1000, stream=None) -> None:
            load_library().egat_selftest_wait_timeout(int(polls), _stream(stream)))
 
 
+@_on_stream
 def egat_eaas_couple_planned(shape: Shape, h: torch.Tensor, plan: torch.Tensor, w: torch.Tensor,
                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Step 2 for the atoms of an attention plan, rotations from its tile records."""
@@ -453,6 +512,7 @@ def egat_eaas_couple_planned(shape: Shape, h: torch.Tensor, plan: torch.Tensor, 
     return out
 
 
+@_on_stream
 def egat_otf_attention_tiled(shape: Shape, q: torch.Tensor, k: torch.Tensor, hp: torch.Tensor,
                              plan: torch.Tensor, w2: Optional[torch.Tensor] = None,
                              fused: bool = True, out: Optional[torch.Tensor] = None,
@@ -468,6 +528,7 @@ def egat_otf_attention_tiled(shape: Shape, q: torch.Tensor, k: torch.Tensor, hp:
     return out
 
 
+@_on_stream
 def egat_forward(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: torch.Tensor,
                  k: torch.Tensor, nbr_or_rowptr: torch.Tensor, cnt_or_col: Optional[torch.Tensor],
                  w1: torch.Tensor, w2: torch.Tensor, order: Optional[torch.Tensor] = None,
@@ -488,6 +549,7 @@ def egat_forward(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: torch.Tens
     return out
 
 
+@_on_stream
 def egat_forward_noalloc(shape: Shape, h: torch.Tensor, pos: torch.Tensor, q: torch.Tensor,
                          k: torch.Tensor, nbr_or_rowptr: torch.Tensor,
                          cnt_or_col: Optional[torch.Tensor], w1: torch.Tensor, w2: torch.Tensor,
@@ -564,30 +626,6 @@ def _elsewhere(dev: int) -> bool:
 def _stream_of(dev: int) -> int:
     """The device's current stream as an integer handle."""
     return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _tensors(*values):
-    """The CUDA tensors among these values."""
-    return [t for t in values if isinstance(t, torch.Tensor) and t.is_cuda]
-
-
-def _moved(f, dev: int, stream, *args):
-    """f(*args) with the tensors' device and the given stream current.  What the call allocates is then
-    that stream's own memory: a block that the caller's stream has given back but may still write is not
-    among it.  Inputs stay allocated until the stream is done with them, results until the caller's stream is."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            return f(*args)
-        if stream.device.index != dev:
-            raise ValueError(f"egat: the stream must belong to CUDA device {dev}, not to {stream.device}")
-        here = torch.cuda.current_stream()
-        with torch.cuda.stream(stream):
-            out = f(*args)
-    for t in _tensors(*args):
-        t.record_stream(stream)
-    for t in _tensors(*out):
-        t.record_stream(here)
-    return out
 
 
 def _scratch(nb: int, workspace: Optional[torch.Tensor], like: torch.Tensor):

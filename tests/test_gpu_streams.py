@@ -5,6 +5,8 @@ caller's references to them as long as a stream uses them."""
 import pytest
 import torch
 
+from equivariant_graph_attention_b200 import synth
+from tests import parity_util
 from tests.molecule_util import make, on_gpu, shape_of
 
 pytestmark = pytest.mark.gpu
@@ -51,7 +53,28 @@ def _norm(seed=0):
     return step, t
 
 
-@pytest.fixture(params=[_attention, _norm], ids=["attention", "norm"])
+def _path(seed=0):
+    """The graph, the projection, the fused forward pass and its gradients of a small system."""
+    egat = _egat()
+    wl = synth.small_cube(80, 9.0, 4.0, 32, 2, 128, 16, 16, "bf16", name="streams80_l2_bf16")
+    shape, t = parity_util.shape_of(wl), parity_util.device_inputs(wl, synth.make(wl))
+    g = torch.Generator("cuda").manual_seed(seed)
+    if seed:
+        t["h"], t["q"] = t["h"].flip(0), t["q"].flip(1)
+    t.update(g=torch.randn((80, 9, 128), generator=g, device="cuda"), wq=torch.randn((128, 256), generator=g, device="cuda"))
+
+    def step(t, stream=None):
+        gr = egat.egat_build_graph(t["pos_q"], wl.cutoff_q, K=wl.K, stream=stream)
+        args = (t["pos"], t["q"], t["k"], gr["nbr"], gr["cnt"], t["w1"], t["w2"])
+        q, k = egat.egat_qk_projection(shape, t["h"], t["wq"], t["wq"], None, None, stream)   # stream by position
+        out = egat.egat_forward(shape, t["h"], *args, order=gr["order"], stream=stream)
+        hp = egat.egat_eaas_couple(shape, t["h"], t["pos"], t["w1"], stream=stream)
+        return [gr["cnt"], gr["order"], q, k, out, hp, egat.egat_gather_rows(t["h"], gr["cnt"], stream=stream),
+                *egat.egat_backward(shape, t["h"], *args, t["g"], order=gr["order"], stream=stream)]
+    return step, t
+
+
+@pytest.fixture(params=[_attention, _norm, _path], ids=["attention", "norm", "path"])
 def case(request):
     step, t = request.param()
     ref = [x.clone() for x in step(t)]
