@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
             um_mma_ts(tmem + 2 * kUmStage, tmem + (i & 1) * kUmStage + w * 32 + k * 8,
                       um_mn_major<kUmStage>(st + L.v + k * 256), um_idesc(L.nv * 8, true), i > 0 || k > 0 || w > 0);
         um_commit(pvdone(i & 1));
-        um_commit(freed(i % kUmStages));
+        // only for a stage that will come: an arrival that nothing waits for could land in
+        // shared memory that the CTA has given up
+        if (i + kUmStages < stages) um_commit(freed(i % kUmStages));
       }
     }
     __syncwarp();
