@@ -469,6 +469,11 @@ int egat_selftest_wait_timeout(int32_t polls, void* stream) {
   return launch_wait_timeout_selftest(polls, static_cast<cudaStream_t>(stream));
 }
 
+int egat_selftest_molecule_wait_timeout(int32_t polls, void* stream) {
+  if (polls < 1 || polls > (1 << 20)) return EGAT_ERR_ARG;
+  return launch_molecule_wait_timeout_selftest(polls, static_cast<cudaStream_t>(stream));
+}
+
 int egat_backward_workspace_bytes(const egat_shape* s, size_t* bytes) {
   if (!bytes) return EGAT_ERR_ARG;
   const int rc = check_shape(s, true);

@@ -167,6 +167,7 @@ struct MolGrads {
   float *dposq, *dposk, *dslope;
 };
 int take_wait_timeouts_molecule(cudaStream_t st, unsigned int* count);
+int launch_molecule_wait_timeout_selftest(int polls, cudaStream_t st);
 size_t molecule_ws_bytes(const egat_mol_shape& s);
 int launch_molecule_attention(const egat_mol_shape& s, const MolArgs& a, void* d_ws, void* d_m,
                               float* d_lse, cudaStream_t st);

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
   um_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(um + L.slot);
 
+  int issued = 0;   // stages whose copies were issued (the copying thread's)
   if (warp == 9) {
     // ---- stages
     const unsigned char* kv = static_cast<const unsigned char*>(p.kv) +
@@ -181,18 +182,10 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
         if (i >= kUmStages && !bounded_wait(freed(s), (i / kUmStages - 1) & 1, kWaitPolls, abort_flag)) break;
         mbar_arrive_expect_tx(full(s), L.key);
         bulk_g2s(base + s * L.key, kv + size_t(i) * L.key, L.key, full(s));
+        issued = i + 1;
       }
     }
     __syncwarp();
-    if (*abort_flag && lane == 0) {   // copies in flight land before the memory is given up
-      volatile int none = 0;
-      if (stages > 0) bounded_wait(qfull, 0, kDrainPolls, &none);
-      for (int s = 0; s < kUmStages; ++s) {
-        int last = stages - 1;
-        while (last >= 0 && last % kUmStages != s) --last;
-        if (last >= 0) bounded_wait(full(s), (last / kUmStages) & 1, kDrainPolls, &none);
-      }
-    }
   } else if (warp == 8) {
     // ---- products
     if (lane == 0 && stages > 0) {
@@ -397,17 +390,43 @@ __global__ void __launch_bounds__(kUmThreads, 2) mol_fwd_umma_kernel(MolParams p
               make_uint4(tc_pack(v[0], v[1]), tc_pack(v[2], v[3]), tc_pack(v[4], v[5]), tc_pack(v[6], v[7]));
       }
   }
-  if (*abort_flag && warp == 8 && lane == 0) {   // products in flight end before tensor memory is freed
-    volatile int none = 0;
-    um_commit(drained);
-    bounded_wait(drained, 0, kDrainPolls, &none);
+  um_release<UmLay::COLS>(abort_flag, 9, 8, drained, tmem, [&](volatile int* none) {
+    if (issued > 0) bounded_wait(qfull, 0, kDrainPolls, none);
+    for (int i = max(0, issued - kUmStages); i < issued; ++i)
+      bounded_wait(full(i % kUmStages), (i / kUmStages) & 1, kDrainPolls, none);
+  });
+}
+
+// The way out of a wait that gives up: a copy is on its way, and a wait for an
+// arrival that never comes runs out of its polls.
+__device__ uint4 g_selftest_source[64];
+__global__ void __launch_bounds__(64) mol_wait_timeout_selftest_kernel(int polls) {
+  __shared__ __align__(128) uint4 to[64];
+  __shared__ __align__(8) uint64_t bar[3];
+  __shared__ uint32_t slot;
+  __shared__ int flag;
+  const uint32_t full = smem_u32(bar), never = smem_u32(bar + 1), drained = smem_u32(bar + 2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(full, 1);
+    mbar_init(never, 1);
+    mbar_init(drained, 1);
+    mbar_fence_init();
+    flag = 0;
   }
+  if (warp == 0) um_alloc<32>(smem_u32(&slot));
   um_before();
   __syncthreads();
-  if (warp == 8) {
-    um_after();
-    um_dealloc<UmLay::COLS>(tmem);
+  um_after();
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(&slot);
+  if (warp == 1 && lane == 0) {
+    mbar_arrive_expect_tx(full, sizeof(to));
+    bulk_g2s(smem_u32(to), g_selftest_source, sizeof(to), full);
+  } else if (warp == 0 && lane == 0) {
+    bounded_wait(never, 0, polls, &flag);
   }
+  __syncwarp();
+  um_release<32>(&flag, 1, 0, drained, tmem, [&](volatile int* none) { bounded_wait(full, 0, kDrainPolls, none); });
 }
 
 }  // namespace
@@ -440,6 +459,10 @@ int mol_umma_forward(const MolParams& p, cudaStream_t st) {
   });
 }
 
+int launch_molecule_wait_timeout_selftest(int polls, cudaStream_t st) {
+  mol_wait_timeout_selftest_kernel<<<1, 64, 0, st>>>(polls);
+  return cudaGetLastError() == cudaSuccess ? EGAT_OK : EGAT_ERR_CUDA;
+}
 int take_wait_timeouts_molecule(cudaStream_t st, unsigned int* count) {
   return take_unit_wait_timeouts(st, count) == 0 ? EGAT_OK : EGAT_ERR_CUDA;
 }

@@ -106,5 +106,31 @@ __device__ __forceinline__ void um_dealloc(uint32_t tmem) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(COLS) : "memory");
 }
 
+// The end of a CTA.  A wait that gave up left copies or products in flight; behind the
+// barrier every role is past its last wait, so the flag no longer changes, and the threads
+// that issued them (lane 0 of two warps; `land` waits for the copies) see them land before
+// shared and tensor memory are given up.  `issuer` is the warp that allocated.
+template <int COLS, typename F>
+__device__ __forceinline__ void um_release(volatile int* abort_flag, int copier, int issuer, uint32_t drained, uint32_t tmem,
+                                           F&& land) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  um_before();
+  __syncthreads();
+  if (*abort_flag) {
+    volatile int none = 0;
+    if (warp == copier && lane == 0) {
+      land(&none);
+    } else if (warp == issuer && lane == 0) {
+      um_commit(drained);
+      bounded_wait(drained, 0, kDrainPolls, &none);
+    }
+    __syncthreads();
+  }
+  if (warp == issuer) {
+    um_after();
+    um_dealloc<COLS>(tmem);
+  }
+}
+
 }  // namespace
 }  // namespace egat

@@ -53,7 +53,7 @@ EXPORTS = ["egat_version", "egat_strerror", "egat_num_paths", "egat_graph_worksp
            "egat_molecule_attention_workspace_bytes", "egat_molecule_attention",
            "egat_molecule_attention_backward_workspace_bytes", "egat_molecule_attention_backward",
            "egat_layer_norm", "egat_layer_norm_backward_workspace_bytes",
-           "egat_layer_norm_backward"]
+           "egat_layer_norm_backward", "egat_selftest_molecule_wait_timeout"]
 
 
 class EgatError(RuntimeError):
@@ -130,6 +130,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.egat_take_device_status.argtypes = [vp]
     lib.egat_selftest_wait_timeout.restype = ctypes.c_int
     lib.egat_selftest_wait_timeout.argtypes = [i32, vp]
+    lib.egat_selftest_molecule_wait_timeout.restype = ctypes.c_int
+    lib.egat_selftest_molecule_wait_timeout.argtypes = [i32, vp]
     lib.egat_eaas_couple_planned.restype = ctypes.c_int
     lib.egat_eaas_couple_planned.argtypes = [sp, vp, vp, vp, vp, vp]
     lib.egat_otf_attention_tiled.restype = ctypes.c_int
@@ -497,6 +499,12 @@ def egat_selftest_wait_timeout(polls: int = 1000, stream=None) -> None:
     """Launch the wait that cannot succeed (see include/egat.h)."""
     _check("egat_selftest_wait_timeout",
            load_library().egat_selftest_wait_timeout(int(polls), _stream(stream)))
+
+
+def egat_selftest_molecule_wait_timeout(polls: int = 1000, stream=None) -> None:
+    """... in a kernel that leaves like the tcgen05 attention within molecules."""
+    _check("egat_selftest_molecule_wait_timeout",
+           load_library().egat_selftest_molecule_wait_timeout(int(polls), _stream(stream)))
 
 
 @_on_stream

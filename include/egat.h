@@ -526,8 +526,9 @@ EGAT_API int egat_gather_rows(const void* d_src, int64_t n_src, int64_t row_byte
 
 /*
  * Device status.  The tensor-core attention kernel, the tile-staged source
- * coupling, the tensor-core query/key projection and the tiled backward
- * passes wait on mbarriers for their bulk copies; every such wait is bounded (about a second).  A wait that
+ * coupling, the tensor-core query/key projection, the tiled backward passes and
+ * the tcgen05 attention within molecules wait on mbarriers for their bulk copies
+ * and products; every such wait is bounded (about a second).  A wait that
  * gives up is counted on the device, the kernel stops waiting and finishes
  * with meaningless output instead of hanging.  The pages have no
  * counterpart: this is the library's failure report.
@@ -543,9 +544,14 @@ EGAT_API int egat_gather_rows(const void* d_src, int64_t n_src, int64_t row_byte
  * `polls` polls (1 .. 1048576), so that egat_take_device_status reports
  * EGAT_ERR_TIMEOUT — a test of the failure path that faults nothing.
  * Asynchronous on `stream`; EGAT_ERR_ARG for polls out of range.
+ *
+ * egat_selftest_molecule_wait_timeout: the same for the tcgen05 attention
+ * within molecules, whose CTAs hold tensor memory and copies in flight when a
+ * wait gives up and leave by the same code as this kernel.
  */
 EGAT_API int egat_take_device_status(void* stream);
 EGAT_API int egat_selftest_wait_timeout(int32_t polls, void* stream);
+EGAT_API int egat_selftest_molecule_wait_timeout(int32_t polls, void* stream);
 
 #ifdef __cplusplus
 }

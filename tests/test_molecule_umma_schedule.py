@@ -1,5 +1,5 @@
 """Host-side model of the barriers of the tcgen05 attention within molecules
-(`mol_fwd_umma_kernel`, csrc/molecule_umma.cu).
+(`mol_fwd_umma_kernel`, csrc/molecule_umma.cu), with waits that give up.
 
 A CTA has a copying thread (stages of keys into three buffers), a thread that
 issues products (scores of stage i into buffer i % 2, then the weights' product
@@ -14,8 +14,9 @@ checks, while no wait gives up:
 * scores never replace weights that a product still reads, and the accumulator is
   rescaled only while no product adds to it;
 
-and that no copy, product or commit is in flight when shared and tensor memory are
-released.  No GPU is involved.
+and always, with waits that give up at random places (what they wait for is late,
+not lost): the roles all end, and when shared and tensor memory are released no
+copy, product or commit is in flight.  No GPU is involved.
 """
 import random
 
@@ -246,6 +247,13 @@ def test_schedules_without_a_give_up(stages):
         Cta(stages, seed, 0.0).run()
 
 
+@pytest.mark.parametrize("stages", [1, 2, 3, 4, 5, 9])
+@pytest.mark.parametrize("rate", [0.3, 0.05, 0.005])
+def test_nothing_in_flight_after_a_give_up(stages, rate):
+    for seed in range(80):
+        Cta(stages, seed, rate).run()
+
+
 def _seen(rates, **rules):
     found = set()
     for rate in rates:
@@ -256,6 +264,12 @@ def _seen(rates, **rules):
                 except Violation as e:
                     found.add(str(e))
     return found
+
+
+def test_a_flag_read_before_the_barrier_is_seen():
+    """A role that looks at the flag when it ends does not see a wait that gives up after it."""
+    found = _seen((0.05, 0.005), late_flag=False)
+    assert "a copy lands in released shared memory" in found and any("in flight when the memory is released" in f for f in found)
 
 
 def test_a_commit_that_nothing_waits_for_is_seen():
