@@ -734,8 +734,10 @@ def egat_molecule_attention_backward(shape: MoleculeShape, q: torch.Tensor, k: t
     dq, dk, dhp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(hp)
     dpos_q = dpos_k = dslope = None
     if slope is not None and positions:
-        dpos_q, dslope = torch.empty_like(pos_q), torch.empty_like(slope)
-        dpos_k = torch.empty_like(pos_k) if k_ptr is not None else None
+        # positions that are missing are the library's to refuse
+        dpos_q = None if pos_q is None else torch.empty_like(pos_q)
+        dpos_k = None if pos_k is None or k_ptr is None else torch.empty_like(pos_k)
+        dslope = torch.empty_like(slope)
     at = [None if t is None else t.data_ptr() for t in (ws, dq, dk, dhp, dpos_q, dpos_k, dslope)]
     rc = load_library().egat_molecule_attention_backward(cs, *ptrs, pm, pl, pg, at[0], nb, *at[1:],
                                                          _stream_of(dev))
