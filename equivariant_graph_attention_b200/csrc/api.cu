@@ -407,6 +407,11 @@ static int check_norm(int64_t ld, int32_t n, int32_t width, int32_t dtype) {
   if (width > 16384) return EGAT_ERR_UNSUPPORTED;
   return ld < width ? EGAT_ERR_ARG : EGAT_OK;
 }
+// In place the rows have to be the same rows: with another stride, a row would be
+// written over one that is still to be read.
+static bool other_rows(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t n) {
+  return a == b && lda != ldb && n > 1;
+}
 static bool aligned_elem(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (storage_bytes(dtype) - 1)) == 0;
 }
@@ -421,6 +426,7 @@ int egat_layer_norm(const void* d_x, int64_t ldx, int32_t n, int32_t width, int3
   if (n == 0) return EGAT_OK;
   if (!d_x || !d_y || !aligned_elem(d_x, dtype) || !aligned_elem(d_y, dtype)) return EGAT_ERR_ARG;
   if (!aligned4(d_weight) || !aligned4(d_bias) || !aligned4(d_stats)) return EGAT_ERR_ARG;
+  if (other_rows(d_x, ldx, d_y, ldy, n)) return EGAT_ERR_ARG;
   return launch_layer_norm(d_x, ldx, n, width, dtype, d_weight, d_bias, eps, d_y, ldy, d_stats,
                            static_cast<cudaStream_t>(stream));
 }
@@ -446,6 +452,7 @@ int egat_layer_norm_backward(const void* d_x, int64_t ldx, int32_t n, int32_t wi
   if (!aligned4(d_weight) || !aligned4(d_stats) || !aligned4(d_dweight) || !aligned4(d_dbias))
     return EGAT_ERR_ARG;
   if (!d_dx && !d_dweight && !d_dbias) return EGAT_OK;
+  if (d_dx && (other_rows(d_grad, ldg, d_dx, lddx, n) || other_rows(d_x, ldx, d_dx, lddx, n))) return EGAT_ERR_ARG;
   const size_t need = layer_norm_backward_ws_bytes(n, width);
   if (need > 0 && (!d_ws || !aligned16(d_ws))) return EGAT_ERR_ARG;
   if (ws_bytes < need) return EGAT_ERR_WORKSPACE;

@@ -485,7 +485,7 @@ EGAT_API int egat_molecule_attention_backward(
  *  ldx, ldy   row strides in elements, >= width
  *  d_weight, d_bias  float32 [width]; NULL = ones, zeros
  *  eps        finite, >= 0
- *  d_y        [n] rows of width; may be d_x itself (in place)
+ *  d_y        [n] rows of width; may be d_x itself (in place, then ldy = ldx)
  *  d_stats    float32 [n][2] (mu, rstd) for the backward pass; may be NULL
  * Mean, centred variance and all sums are float32.  n = 0 is a no-op.
  *
@@ -493,7 +493,8 @@ EGAT_API int egat_molecule_attention_backward(
  * upstream gradient g, with xh = (x - mu) rstd and t = g weight,
  *   dx = rstd (t - mean_c t - xh mean_c(t xh)),
  *   dweight[c] = sum_i g_i[c] xh_i[c],  dbias[c] = sum_i g_i[c]
- *  d_dx       row stride lddx; may be NULL, and may be the gradient's rows
+ *  d_dx       row stride lddx; may be NULL, and may be the gradient's or x's
+ *             rows (in place, then with their stride)
  *  d_dweight, d_dbias  float32 [width]; may be NULL.  n = 0 gives zeros
  *  d_ws       at least egat_layer_norm_backward_workspace_bytes(n, width)
  * The weight sums run in a fixed order (per-block partial sums, then one

@@ -28,3 +28,16 @@ def egat_call(polls):
     class Stream:
         cuda_stream = None
     egat.egat_selftest_molecule_wait_timeout(polls, Stream())
+
+
+def test_in_place_norm_of_other_rows_refused(lib):
+    """Another stride over the same start would write rows that are still to be read."""
+    f, b = lib.egat_layer_norm, lib.egat_layer_norm_backward
+    OTHER, WS = ctypes.c_void_p(0x20000), ctypes.c_void_p(0x40000)
+    # x, ldx, n, width, dtype, weight, bias, eps, y, ldy, stats, stream
+    assert f(OK, 256, 10, 128, 1, None, None, 1e-5, OK, 128, None, None) == egat.EGAT_ERR_ARG
+    assert f(OK, 128, 10, 128, 1, None, None, 1e-5, OK, 256, None, None) == egat.EGAT_ERR_ARG
+    # x, ldx, n, width, dtype, weight, stats, grad, ldg, ws, ws_bytes, dx, lddx, dweight, dbias, stream
+    for x, grad in ((OTHER, OK), (OK, OTHER)):
+        for ld, lddx in ((256, 128), (128, 256)):
+            assert b(x, ld, 10, 128, 1, None, WS, grad, ld, WS, 1 << 30, OK, lddx, None, None, None) == egat.EGAT_ERR_ARG
