@@ -422,15 +422,19 @@ EGAT_API int egat_escn_conv(const egat_shape* s, int32_t mmax, const void* d_h, 
  *  d_lse    float32 [nq][H], natural logarithm; may be NULL (the backward
  *           pass needs it)
  *  d_ws     at least egat_molecule_attention_workspace_bytes(s): none for short
- *           molecules, the operands laid out by head for long ones of bf16 (about
+ *           molecules, the operands laid out by head for the tcgen05 kernels (about
  *           nk * (H dk + D C) * 2 bytes), the parts of a key split for few queries
  *  limits   nq and nk up to 2^30, n_mol up to 2^28
- * Feature and workspace pointers are 16-byte aligned.  Sums and softmax
- * statistics are float32, and products of float32 storage carry 24 bits (an
- * infinite float32 value gives NaN where its weight is not zero, too).
- * Deterministic.  nq = 0 is a no-op.  Molecules of 512 atoms and more on
- * average, of bf16, run on tcgen05 kernels whose bounded waits report through
- * egat_take_device_status.
+ * Feature and workspace pointers are 16-byte aligned; outputs overlap no input.
+ * Sums and softmax statistics are float32, and products of float32 storage carry
+ * 24 bits.  Up to 144 value columns a head these are products of three bf16
+ * parts, where an infinite value, or one above 3.38e38 (whose first part is
+ * infinite), gives NaN in every row that its product enters, with a weight of
+ * zero too; wider heads keep such values as float32 does.
+ * Deterministic.  nq = 0 is a no-op.  The forward pass runs on tcgen05 kernels,
+ * whose bounded waits report through egat_take_device_status, for bf16 with at
+ * most 128 value columns a head (D C / H), 512 rows a molecule on average on both
+ * sides and (nq / 128 + n_mol) H >= 96 (one system of 640 atoms with 16 heads).
  *
  * egat_molecule_attention_backward: for an upstream gradient G = dL/dm
  * ([nq][D][C] in s->dtype, 16-byte aligned) and the forward's m and lse,

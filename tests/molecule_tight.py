@@ -28,3 +28,13 @@ def tight(d, o):
         if x in o:
             out[x] = (f32[x] + planes * P * o["abs_" + x]) * (1 + B) + B * np.abs(o[x])
     return out
+
+
+def packed_bytes(shape):
+    """Workspace of the forward pass where it takes the tcgen05 kernels: keys, values and positions in blocks of
+    64 rows of a head, queries in blocks of 128, a block for every slot that a row tile can have."""
+    up = lambda x, m: (x + m - 1) // m * m
+    dv, ks = shape.D * shape.C // shape.H, 2 if shape.dk > 16 else 1
+    key = 64 * 16 * (2 * ks + up(dv // 8, 2) + 1)
+    slots = lambda n, rows: n // rows + shape.n_mol + 2
+    return up(slots(shape.nk, 64) * shape.H * key, 256) + up(slots(shape.nq, 128) * shape.H * 2 * ks * 128 * 16, 256)

@@ -41,3 +41,20 @@ def test_in_place_norm_of_other_rows_refused(lib):
     for x, grad in ((OTHER, OK), (OK, OTHER)):
         for ld, lddx in ((256, 128), (128, 256)):
             assert b(x, ld, 10, 128, 1, None, WS, grad, ld, WS, 1 << 30, OK, lddx, None, None, None) == egat.EGAT_ERR_ARG
+
+
+BASE = dict(nq=1024, nk=1024, n_mol=2, lmax=2, C=128, H=16, dk=16, dtype="bf16", cap=0.0)
+
+
+@pytest.mark.parametrize("kw,takes", [
+    ({}, True), (dict(dtype="f32"), False), (dict(nk=1023), False), (dict(nq=1023), False), (dict(n_mol=3), False),
+    (dict(nk=1 << 20), True), (dict(n_mol=1), True), (dict(n_mol=1, nq=640, nk=640), True),
+    (dict(n_mol=1, nq=639), False), (dict(n_mol=1, H=8, C=64, nq=1408, nk=1408), True),
+    (dict(n_mol=1, H=8, C=64, nq=1407, nk=1407), False), (dict(lmax=3), True), (dict(H=8, nq=2048, nk=2048), False),
+    (dict(H=8, lmax=1, nq=2048, nk=2048), True), (dict(n_mol=0), False)], ids=str)
+def test_which_shapes_take_the_tcgen05_kernels(lib, kw, takes):
+    """bf16, at most 128 value columns a head, 512 rows a molecule on average on both sides, (nq / 128 + n_mol) H of 96
+    at least: by the workspace, which is that of the packed operands there and nowhere else."""
+    from tests.molecule_tight import packed_bytes
+    s = egat.MoleculeShape(**dict(BASE, **kw))
+    assert (egat.egat_molecule_attention_workspace_bytes(s) == packed_bytes(s)) is takes
