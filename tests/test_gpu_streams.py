@@ -146,3 +146,17 @@ def test_streams_of_another_device_are_refused():
         device, cuda_stream = torch.device("cuda", 1), 0
     with pytest.raises(ValueError):
         step(t, Elsewhere())
+
+
+def test_captured_on_the_stream_that_is_passed(case):
+    step, t, ref, _ = case
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    step(t, s)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(t, s)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        assert _equal(got, ref)
