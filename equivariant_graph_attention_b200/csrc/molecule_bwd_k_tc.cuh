@@ -8,7 +8,7 @@ namespace egat {
 namespace {
 
 // Bound by latency at two blocks an SM: the accumulators and the key rows' fragments
-// fill the registers (4,096 atoms capped: 0.73 ms, a third of the tensor pipe and of
+// fill the registers (4,096 atoms capped: 0.73 ms, 39 % of the tensor pipe, a third of
 // the issue slots).
 //
 // dL/dk, dL/dh' and, with POS, the key side of dL/dr: a warp owns 16 key rows

@@ -360,7 +360,9 @@ __global__ void __launch_bounds__(kTcThreads, PL == 1 && NT * HP <= 9 ? (POS ? 3
 }
 
 // One head a warp at 72 columns: three or four blocks an SM instead of two (4,096
-// atoms capped: 0.61 -> 0.52 ms; the key side and the forward pass lose by it).  Bound
+// atoms capped: 0.61 -> 0.52 ms; the key side and the forward pass lose by it).  Two heads
+// of up to 32 columns fall under the same bound, unmeasured, and spill (340 bytes a thread,
+// 980 with position gradients).  Bound
 // by instruction issue and latency: half of the issue slots are busy, a quarter of
 // the tensor pipe.
 template <int PL>

@@ -20,9 +20,8 @@
 // other CTA's products.  Work per pair and head is one exponential (and one
 // root with a bias) on the special-function unit (8,191 atoms, lmax 3: 0.24 of 0.64 ms);
 // cap and bias add 13 operations on the FMA pipe and bound it there (4,096 atoms, lmax 2:
-// 0.17 of 0.37 ms).  The products take two thirds of the exponentials' time at 72 value
-// columns and as much as they at 128 (16 + 2 x 128 columns a pair: 0.33 ms at the measured
-// rate), where they bound it.  One plane of the weights took 0.35 and 0.46 ms for these
+// 0.17 of 0.37 ms).  The products take 0.05 ms at the measured rate in the second case and
+// 0.35 ms in the first (16 + 2 x 128 columns a pair), where they bound it.  One plane of the weights took 0.46 and 0.35 ms for these
 // two, with an error of m up to 1.4 times that of its own rounding.  Every wait is bounded.
 #include <algorithm>
 
